@@ -271,6 +271,136 @@ muon_status adamw_step_clipped_noalloc(muon_handle h, const adamw_tensor* ts, in
                                        const adamw_hparams* hp, float max_norm,
                                        float* norm_out, void* stream);
 
+/* ---- what the step consumes ------------------------------------------------
+ * Operators on the step's inputs: one gradient norm over every tensor and the
+ * clip to it, the products of a mixture-of-experts layer (whose weight
+ * gradients are Muon matrices, one per expert), and the largest attention
+ * logit per head for QK-Clip.  They follow the rules above: caller-owned
+ * device memory, validation before anything is enqueued, work on `stream`
+ * only, no wait on the host, capture allowed.  Group sizes and sequence
+ * lengths are device data that the host never reads. */
+
+/* One gradient tensor: rows x cols, row-major with leading dimension ld_grad
+ * (elements, >= cols), F32 or BF16.  A vector is one row.  rows or cols may
+ * be 0 (nothing to add).  out (muon_grad_clip only): receives the clipped
+ * gradient, F32 or BF16 with leading dimension ld_out; out == grad with the
+ * same type and leading dimension clips in place. */
+typedef struct {
+    const void* grad;
+    void* out;
+    int64_t rows, cols;
+    int64_t ld_grad, ld_out;
+    int32_t grad_dtype; /* muon_dtype */
+    int32_t out_dtype;  /* muon_dtype */
+} muon_grad;
+
+/* Bytes of workspace for muon_grad_norm and muon_grad_clip over n tensors. */
+muon_status muon_grad_workspace_size(muon_handle h, const muon_grad* gs, int n, size_t* bytes);
+
+/* Global Euclidean norm over all elements of all n tensors, and the clip
+ * scale: max_norm / norm if norm > max_norm, else 1 (adamw_step_clipped's
+ * rule).  norm_out, scale_out: optional device floats (one of them at least).
+ * Squares are formed and summed in 64 bits in a fixed order: results are
+ * bitwise repeatable, and no gradient is too large or too small for its
+ * square.  A NaN norm clips nothing, an infinite one scales by 0.  A tensor
+ * listed twice counts twice.  muon_step_batched_scaled and adamw_step_scaled
+ * take scale_out as it is, so that one norm over Muon and AdamW tensors clips
+ * both steps without a clipped copy.
+ * workspace: muon_grad_workspace_size bytes, 256-byte aligned, not shared by
+ * calls that may overlap in time.  Rejects n < 1, negative sizes, ld < cols,
+ * a null grad, unknown dtypes, max_norm <= 0 or non-finite, a small or null
+ * workspace. */
+muon_status muon_grad_norm(muon_handle h, const muon_grad* gs, int n, float max_norm,
+                           float* norm_out, float* scale_out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* The same, then out = grad * scale for every tensor, rounded once to out's
+ * type.  Also rejects a null out, and outputs that share memory with another
+ * tensor's gradient or output, or with their own gradient other than exactly
+ * in place (MUON_ERR_OVERLAP). */
+muon_status muon_grad_clip(muon_handle h, const muon_grad* gs, int n, float max_norm,
+                           float* norm_out, float* scale_out, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* muon_step_batched and adamw_step with every gradient multiplied by the
+ * device float *grad_scale first (read when the step runs; the gradient
+ * tensors are not modified).  grad_scale may not lie in the workspace. */
+muon_status muon_step_batched_scaled(muon_handle h, const muon_matrix* mats, int n,
+                                     const muon_hparams* hp, const float* grad_scale,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+muon_status adamw_step_scaled(muon_handle h, const adamw_tensor* ts, int n,
+                              const adamw_hparams* hp, const float* grad_scale, void* stream);
+
+/* Matrices of a layer's experts: `experts` (at most 1024) device pointers in a
+ * HOST array, read during the call only, each rows x cols = (fan-out, fan-in)
+ * row-major with leading dimension ld.  dtype: theirs. */
+typedef struct {
+    const void* const* weights;
+    int64_t rows, cols, ld;
+    int32_t experts;
+    int32_t dtype; /* muon_dtype */
+} muon_experts;
+
+/* Products grouped by expert.  Rows offsets[e] ... offsets[e + 1] - 1 of the
+ * token tensors belong to expert e (offsets: experts + 1 device int32,
+ * ascending, within [0, tokens]; a group may be empty).  Token tensors are
+ * row-major, `tokens` rows, leading dimensions in elements.
+ *   forward       y  = x W_e^T    x tokens x cols, y tokens x rows
+ *   grad_input    dx = dy W_e     dy tokens x rows, dx tokens x cols
+ *   grad_weight   dW_e = dy^T x over the rows of group e, or dW_e += with
+ *                 accumulate; an empty group's dW_e is set to zero, or left
+ *                 as it is with accumulate
+ * All in the weights' dtype (forward, grad_input) or with x and dy in `dtype`
+ * and dW in grads->dtype (grad_weight; BF16 x and dy with BF16 or F32
+ * gradients, F32 with F32); sums in fp32, rounded once.  Rows of y and dx
+ * outside every group are left as they are.  Offsets that are not ascending
+ * or leave [0, tokens] are clamped: no access leaves the tensors, and what
+ * rows get is then unspecified.  Rejects experts, sizes or leading dimensions
+ * out of range, null pointers, and outputs that share memory with anything
+ * else of the call. */
+muon_status muon_expert_forward(muon_handle h, const muon_experts* ex, const int32_t* offsets,
+                                const void* x, int64_t ld_x, void* y, int64_t ld_y, int64_t tokens,
+                                void* stream);
+muon_status muon_expert_grad_input(muon_handle h, const muon_experts* ex, const int32_t* offsets,
+                                   const void* dy, int64_t ld_dy, void* dx, int64_t ld_dx,
+                                   int64_t tokens, void* stream);
+muon_status muon_expert_grad_weight(muon_handle h, const muon_experts* grads, const int32_t* offsets,
+                                    const void* x, int64_t ld_x, const void* dy, int64_t ld_dy,
+                                    int64_t tokens, int32_t dtype, int accumulate, void* stream);
+
+/* Queries and keys of one attention layer, packed sequences: element d of head
+ * h of token t at q[t * q_token + h * q_head + d] (strides in elements), F32 or
+ * BF16 both.  Query head h reads key head h / (heads_q / heads_k).  Sequence s
+ * has queries cu_q[s] ... cu_q[s + 1] - 1 and keys cu_k[s] ... cu_k[s + 1] - 1
+ * (device int32, sequences + 1 each, clamped like the experts' offsets).
+ * causal: query i of Lq sees keys j <= i + (Lk - Lq). */
+typedef struct {
+    const void* q;
+    const void* k;
+    int64_t tokens_q, tokens_k;
+    int64_t q_token, q_head, k_token, k_head;
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+    int32_t sequences;
+    int32_t heads_q, heads_k, head_dim;
+    int32_t dtype;  /* muon_dtype */
+    int32_t causal; /* 0 or 1 */
+    float scale;    /* > 0, typically 1 / sqrt(head_dim) */
+} muon_qk;
+
+/* S_h = the largest scale * <q_i, k_j> over all sequences and unmasked pairs,
+ * the values muon_matrix.qk_smax takes: smax_q (heads_q floats) for the query
+ * projection, smax_k (heads_k floats, the largest of the query heads that
+ * share the key head) for the key projection; either may be null.  Products
+ * are summed in fp32.  -inf where a head has no unmasked pair, NaN where one
+ * of its unmasked logits is; masked pairs never count.  accumulate: the larger
+ * of the result and what the output holds (micro-batches).
+ * workspace: as above, muon_qk_smax_workspace_size bytes (it depends on the
+ * sizes, not on pointers). */
+muon_status muon_qk_smax_workspace_size(muon_handle h, const muon_qk* qk, size_t* bytes);
+muon_status muon_qk_smax(muon_handle h, const muon_qk* qk, float* smax_q, float* smax_k,
+                         int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static, human readable name of a status. */
 const char* muon_status_str(muon_status s);
 

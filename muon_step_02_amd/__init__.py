@@ -10,10 +10,15 @@ Names follow the C ABI in ``include/muon.h``:
 * :func:`muon_workspace_size`
 * :func:`muon_step_batched`
 * :func:`adamw_step`
+* :func:`muon_grad_norm`, :func:`muon_grad_clip` and the steps that take their
+  scale, :func:`muon_step_batched_scaled`, :func:`adamw_step_scaled`
+* :func:`muon_expert_forward`, :func:`muon_expert_grad_input`,
+  :func:`muon_expert_grad_weight`
+* :func:`muon_qk_smax`
 
 plus helpers that build the C descriptors from PyTorch tensors
 (:func:`muon_matrix`, :func:`muon_hparams`, :func:`adamw_tensor`,
-:func:`adamw_hparams`).
+:func:`adamw_hparams`, :func:`muon_grad`, :func:`muon_experts`).
 """
 
 from ._lib import (  # noqa: F401
@@ -22,6 +27,9 @@ from ._lib import (  # noqa: F401
     MUON_F32,
     SCALE_MODES,
     MuonError,
+    MuonExperts,
+    MuonGrad,
+    MuonQk,
     AdamwHparams,
     AdamwTensor,
     MuonHparams,
@@ -30,11 +38,20 @@ from ._lib import (  # noqa: F401
     adamw_step,
     adamw_step_clipped,
     adamw_step_clipped_noalloc,
+    adamw_step_scaled,
     adamw_workspace_size,
     adamw_tensor,
     exported_symbols,
     load,
     muon_destroy,
+    muon_expert_forward,
+    muon_expert_grad_input,
+    muon_expert_grad_weight,
+    muon_experts,
+    muon_grad,
+    muon_grad_clip,
+    muon_grad_norm,
+    muon_grad_workspace_size,
     muon_hparams,
     muon_init,
     muon_matrix,
@@ -42,7 +59,10 @@ from ._lib import (  # noqa: F401
     muon_profile_enable,
     PhaseTimes,
     PHASES,
+    muon_qk_smax,
+    muon_qk_smax_workspace_size,
     muon_step_batched,
+    muon_step_batched_scaled,
     muon_test_gram_bf16,
     muon_test_poly_bf16,
     muon_test_update_bf16,

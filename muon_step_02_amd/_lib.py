@@ -37,6 +37,16 @@ SYMBOLS = (
     "adamw_step_clipped",
     "muon_test_split_matrices",
     "adamw_step_clipped_noalloc",
+    "muon_step_batched_scaled",
+    "adamw_step_scaled",
+    "muon_grad_workspace_size",
+    "muon_grad_norm",
+    "muon_grad_clip",
+    "muon_expert_forward",
+    "muon_expert_grad_input",
+    "muon_expert_grad_weight",
+    "muon_qk_smax_workspace_size",
+    "muon_qk_smax",
 )
 
 NUM_PHASES = 7
@@ -111,6 +121,52 @@ class AdamwHparams(ctypes.Structure):
     ]
 
 
+class MuonGrad(ctypes.Structure):
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld_grad", ctypes.c_int64),
+        ("ld_out", ctypes.c_int64),
+        ("grad_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+    ]
+
+
+class MuonExperts(ctypes.Structure):
+    _fields_ = [
+        ("weights", ctypes.POINTER(ctypes.c_void_p)),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("experts", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class MuonQk(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p),
+        ("k", ctypes.c_void_p),
+        ("tokens_q", ctypes.c_int64),
+        ("tokens_k", ctypes.c_int64),
+        ("q_token", ctypes.c_int64),
+        ("q_head", ctypes.c_int64),
+        ("k_token", ctypes.c_int64),
+        ("k_head", ctypes.c_int64),
+        ("cu_q", ctypes.c_void_p),
+        ("cu_k", ctypes.c_void_p),
+        ("sequences", ctypes.c_int32),
+        ("heads_q", ctypes.c_int32),
+        ("heads_k", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 _lib = None
 
 
@@ -146,13 +202,30 @@ def load():
                                              ctypes.POINTER(ctypes.c_int)]
     lib.adamw_step_clipped_noalloc.argtypes = [vp, ctypes.POINTER(AdamwTensor), i32,
                                                ctypes.POINTER(AdamwHparams), f32, vp, vp]
+    sz = ctypes.c_size_t
+    lib.muon_step_batched_scaled.argtypes = [vp, ctypes.POINTER(MuonMatrix), i32,
+                                             ctypes.POINTER(MuonHparams), vp, vp, sz, vp]
+    lib.adamw_step_scaled.argtypes = [vp, ctypes.POINTER(AdamwTensor), i32,
+                                      ctypes.POINTER(AdamwHparams), vp, vp]
+    lib.muon_grad_workspace_size.argtypes = [vp, ctypes.POINTER(MuonGrad), i32, ctypes.POINTER(sz)]
+    for name in ("muon_grad_norm", "muon_grad_clip"):
+        getattr(lib, name).argtypes = [vp, ctypes.POINTER(MuonGrad), i32, f32, vp, vp, vp, sz, vp]
+    for name in ("muon_expert_forward", "muon_expert_grad_input"):
+        getattr(lib, name).argtypes = [vp, ctypes.POINTER(MuonExperts), vp, vp, i64, vp, i64, i64, vp]
+    lib.muon_expert_grad_weight.argtypes = [vp, ctypes.POINTER(MuonExperts), vp, vp, i64, vp, i64,
+                                            i64, ctypes.c_int32, i32, vp]
+    lib.muon_qk_smax_workspace_size.argtypes = [vp, ctypes.POINTER(MuonQk), ctypes.POINTER(sz)]
+    lib.muon_qk_smax.argtypes = [vp, ctypes.POINTER(MuonQk), vp, vp, i32, vp, sz, vp]
     lib.muon_profile_enable.argtypes = [vp, i32]
     lib.muon_profile_collect.argtypes = [vp, ctypes.POINTER(PhaseTimes)]
     for name in ("muon_init", "muon_destroy", "muon_workspace_size", "muon_step_batched",
                  "adamw_step", "muon_test_gram_bf16", "muon_test_poly_bf16",
                  "muon_test_update_bf16", "muon_profile_enable", "muon_profile_collect",
                  "adamw_workspace_size", "adamw_step_clipped", "muon_test_split_matrices",
-                 "adamw_step_clipped_noalloc"):
+                 "adamw_step_clipped_noalloc", "muon_step_batched_scaled", "adamw_step_scaled",
+                 "muon_grad_workspace_size", "muon_grad_norm", "muon_grad_clip",
+                 "muon_expert_forward", "muon_expert_grad_input", "muon_expert_grad_weight",
+                 "muon_qk_smax_workspace_size", "muon_qk_smax"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -334,6 +407,241 @@ def adamw_step_clipped_noalloc(h, tensors, hp, max_norm, norm_out=None, stream=N
         h, arr, len(tensors), ctypes.byref(hp), float(max_norm),
         ctypes.c_void_p(norm_out.data_ptr() if norm_out is not None else 0), _stream_ptr(stream)),
         "adamw_step_clipped_noalloc")
+
+
+def _same_device(*tensors):
+    """The one CUDA device of the tensors (None among them: not given)."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError("expected tensors on one CUDA device, got %s" % sorted(map(str, devices)))
+    return devices.pop()
+
+
+def _stream_on(stream, device):
+    """`stream`, or the current stream of the tensors' device."""
+    if stream is None:
+        import torch
+        stream = torch.cuda.current_stream(device)
+    return _stream_ptr(stream)
+
+
+def _scalar(t, what):
+    import torch
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise ValueError("%s must be one float32" % what)
+    return t.data_ptr()
+
+
+def _nbytes(workspace):
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.numel() * workspace.element_size()
+
+
+def _int32(t, what):
+    import torch
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous 1D int32 tensor" % what)
+    return t.data_ptr()
+
+
+def muon_step_batched_scaled(h, mats, hp, grad_scale, workspace, stream=None):
+    """:func:`muon_step_batched` with every gradient multiplied by the one-element
+    float32 CUDA tensor ``grad_scale`` (:func:`muon_grad_norm`'s ``scale_out``)."""
+    arr = _array(mats)
+    dev = _same_device(grad_scale, workspace)
+    _check(load().muon_step_batched_scaled(h, arr, len(mats), ctypes.byref(hp),
+                                           _scalar(grad_scale, "grad_scale"), workspace.data_ptr(),
+                                           _nbytes(workspace), _stream_on(stream, dev)),
+           "muon_step_batched_scaled")
+
+
+def adamw_step_scaled(h, tensors, hp, grad_scale, stream=None):
+    """:func:`adamw_step` with every gradient multiplied by ``grad_scale``."""
+    arr = (AdamwTensor * len(tensors))(*tensors)
+    dev = _same_device(grad_scale)
+    _check(load().adamw_step_scaled(h, arr, len(tensors), ctypes.byref(hp),
+                                    _scalar(grad_scale, "grad_scale"), _stream_on(stream, dev)),
+           "adamw_step_scaled")
+
+
+def _rows_of(t):
+    """(rows, cols, leading dimension) of a vector, of a matrix with unit
+    column stride, or of a contiguous tensor of any shape."""
+    if t.dim() == 2 and t.numel() and (t.stride(1) == 1 or t.shape[1] == 1) and \
+            (t.stride(0) >= t.shape[1] or t.shape[0] == 1):
+        return t.shape[0], t.shape[1], t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor, or a 2D one with stride(1) == 1")
+    return 1, t.numel(), t.numel()
+
+
+def muon_grad(grad, out=None):
+    """Descriptor of one gradient for :func:`muon_grad_norm` and, with ``out``
+    (the gradient itself clips in place), :func:`muon_grad_clip`."""
+    rows, cols, ld = _rows_of(grad)
+    g = MuonGrad(grad=grad.data_ptr(), rows=rows, cols=cols, ld_grad=ld, grad_dtype=_dt(grad))
+    if out is not None:
+        if out.shape != grad.shape:
+            raise ValueError("grad and out shapes differ")
+        orows, ocols, old = _rows_of(out)
+        if (orows, ocols) != (rows, cols):
+            # one of the two is seen as one row: both are then
+            if not (grad.is_contiguous() and out.is_contiguous()):
+                raise ValueError("grad and out layouts differ")
+            g.rows, g.cols, g.ld_grad, old = 1, grad.numel(), grad.numel(), grad.numel()
+        g.out, g.ld_out, g.out_dtype = out.data_ptr(), old, _dt(out)
+    return g
+
+
+def muon_grad_workspace_size(h, grads):
+    arr = (MuonGrad * len(grads))(*grads)
+    sz = ctypes.c_size_t()
+    _check(load().muon_grad_workspace_size(h, arr, len(grads), ctypes.byref(sz)),
+           "muon_grad_workspace_size")
+    return sz.value
+
+
+def _grad_call(name, h, grads, max_norm, workspace, norm_out, scale_out, stream):
+    arr = grads if isinstance(grads, ctypes.Array) else (MuonGrad * len(grads))(*grads)
+    dev = _same_device(workspace, norm_out, scale_out)
+    _check(getattr(load(), name)(h, arr, len(arr), float(max_norm), _scalar(norm_out, "norm_out"),
+                                 _scalar(scale_out, "scale_out"), workspace.data_ptr(),
+                                 _nbytes(workspace), _stream_on(stream, dev)), name)
+
+
+def muon_grad_norm(h, grads, max_norm, workspace, norm_out=None, scale_out=None, stream=None):
+    """Global norm of all ``grads`` (:func:`muon_grad` descriptors) and the clip
+    scale for ``max_norm``, into one-element float32 CUDA tensors."""
+    _grad_call("muon_grad_norm", h, grads, max_norm, workspace, norm_out, scale_out, stream)
+
+
+def muon_grad_clip(h, grads, max_norm, workspace, norm_out=None, scale_out=None, stream=None):
+    """:func:`muon_grad_norm`, then every descriptor's ``out`` = ``grad`` * scale."""
+    _grad_call("muon_grad_clip", h, grads, max_norm, workspace, norm_out, scale_out, stream)
+
+
+def muon_experts(weights):
+    """Descriptor of a layer's expert matrices (or their gradients): equally
+    shaped 2D tensors of one type and leading dimension."""
+    if not weights:
+        raise ValueError("no experts")
+    w0 = weights[0]
+    dev = _same_device(*weights)
+    ld = _ld(w0) if w0.shape[0] > 1 else w0.shape[1]
+    for w in weights:
+        if w.shape != w0.shape or w.dtype != w0.dtype or (w.shape[0] > 1 and _ld(w) != ld):
+            raise ValueError("the experts' shapes, types or leading dimensions differ")
+    ptrs = (ctypes.c_void_p * len(weights))(*[w.data_ptr() for w in weights])
+    ex = MuonExperts(weights=ptrs, rows=w0.shape[0], cols=w0.shape[1], ld=ld, experts=len(weights),
+                     dtype=_dt(w0))
+    ex._keepalive = (ptrs, list(weights))
+    ex._device = dev
+    return ex
+
+
+def _tokens(t, width, what):
+    """Pointer and leading dimension of a token tensor of `width` columns."""
+    if t.dim() != 2 or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be 2D with %d columns and unit column stride" % (what, width))
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def _offsets(ex, offsets, *tensors):
+    if offsets.numel() != ex.experts + 1:
+        raise ValueError("offsets must hold experts + 1 values")
+    dev = _same_device(offsets, *tensors)
+    if dev != ex._device:
+        raise ValueError("the experts are on %s, the tokens on %s" % (ex._device, dev))
+    return _int32(offsets, "offsets"), dev
+
+
+def _expert_rows(name, h, ex, offsets, x, y, wx, wy, stream):
+    po, dev = _offsets(ex, offsets, x, y)
+    if _dt(x) != ex.dtype or _dt(y) != ex.dtype:
+        raise TypeError("tokens and weights differ in type")
+    if x.shape[0] != y.shape[0]:
+        raise ValueError("the token tensors differ in rows")
+    px, lx = _tokens(x, wx, "the input")
+    py, ly = _tokens(y, wy, "the output")
+    _check(getattr(load(), name)(h, ctypes.byref(ex), po, px, lx, py, ly, x.shape[0],
+                                 _stream_on(stream, dev)), name)
+
+
+def muon_expert_forward(h, ex, offsets, x, y, stream=None):
+    """y[t] = W_e x[t] for the rows t of every group e: ``offsets`` (experts + 1
+    int32, CUDA) bounds the groups; other rows of ``y`` stay as they are."""
+    _expert_rows("muon_expert_forward", h, ex, offsets, x, y, ex.cols, ex.rows, stream)
+
+
+def muon_expert_grad_input(h, ex, offsets, dy, dx, stream=None):
+    """dx[t] = W_e^T dy[t], the input gradient of :func:`muon_expert_forward`."""
+    _expert_rows("muon_expert_grad_input", h, ex, offsets, dy, dx, ex.rows, ex.cols, stream)
+
+
+def muon_expert_grad_weight(h, grads, offsets, x, dy, accumulate=False, stream=None):
+    """dW_e = sum of dy[t] x[t]^T over the rows of group e, or += with
+    ``accumulate``; ``grads``: :func:`muon_experts` of the gradient tensors."""
+    po, dev = _offsets(grads, offsets, x, dy)
+    if _dt(x) != _dt(dy):
+        raise TypeError("x and dy differ in type")
+    if x.shape[0] != dy.shape[0]:
+        raise ValueError("the token tensors differ in rows")
+    px, lx = _tokens(x, grads.cols, "x")
+    pd, ldd = _tokens(dy, grads.rows, "dy")
+    _check(load().muon_expert_grad_weight(h, ctypes.byref(grads), po, px, lx, pd, ldd, x.shape[0],
+                                          _dt(x), 1 if accumulate else 0, _stream_on(stream, dev)),
+           "muon_expert_grad_weight")
+
+
+def _qk(q, k, cu_q, cu_k, scale, causal):
+    if q.dim() != 3 or k.dim() != 3 or q.shape[2] != k.shape[2]:
+        raise ValueError("q and k must be (tokens, heads, head_dim) with equal head_dim")
+    if q.shape[2] > 1 and (q.stride(2) != 1 or k.stride(2) != 1):
+        raise ValueError("q and k need unit stride in their last dimension")
+    if _dt(q) != _dt(k):
+        raise TypeError("q and k differ in type")
+    if cu_q is not None and cu_k is not None and cu_q.numel() != cu_k.numel():
+        raise ValueError("cu_q and cu_k differ in length")
+    if cu_q.numel() < 2:
+        raise ValueError("cu_q must hold sequences + 1 values")
+    return MuonQk(q=q.data_ptr(), k=k.data_ptr(), tokens_q=q.shape[0], tokens_k=k.shape[0],
+                  q_token=q.stride(0), q_head=q.stride(1), k_token=k.stride(0), k_head=k.stride(1),
+                  cu_q=_int32(cu_q, "cu_q"), cu_k=_int32(cu_k, "cu_k") if cu_k is not None else None,
+                  sequences=cu_q.numel() - 1, heads_q=q.shape[1], heads_k=k.shape[1],
+                  head_dim=q.shape[2], dtype=_dt(q), causal=1 if causal else 0,
+                  scale=q.shape[2] ** -0.5 if scale is None else float(scale))
+
+
+def muon_qk_smax_workspace_size(h, q, k, cu_q):
+    """Workspace bytes of :func:`muon_qk_smax` for tensors of these shapes."""
+    sz = ctypes.c_size_t()
+    qk = _qk(q, k, cu_q, None, None, True)
+    _check(load().muon_qk_smax_workspace_size(h, ctypes.byref(qk), ctypes.byref(sz)),
+           "muon_qk_smax_workspace_size")
+    return sz.value
+
+
+def muon_qk_smax(h, q, k, cu_q, cu_k, smax_q, workspace, smax_k=None, scale=None, causal=True,
+                 accumulate=False, stream=None):
+    """Largest logit scale * <q_i, k_j> per head over packed sequences: ``q``
+    (tokens, heads, head_dim), ``k`` (tokens, key heads, head_dim), ``cu_q`` and
+    ``cu_k`` the sequences' bounds (int32, CUDA).  ``smax_q`` and ``smax_k``
+    (float32, one value per head; either may be None) are what
+    :func:`muon_matrix` takes as ``qk_smax`` for the query and the key
+    projection.  ``scale`` defaults to head_dim ** -0.5."""
+    import torch
+    dev = _same_device(q, k, cu_q, cu_k, smax_q, smax_k, workspace)
+    for t, n in ((smax_q, q.shape[1]), (smax_k, k.shape[1])):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
+            raise ValueError("smax outputs must be contiguous float32, one value per head")
+    qk = _qk(q, k, cu_q, cu_k, scale, causal)
+    _check(load().muon_qk_smax(h, ctypes.byref(qk), smax_q.data_ptr() if smax_q is not None else None,
+                               smax_k.data_ptr() if smax_k is not None else None,
+                               1 if accumulate else 0, workspace.data_ptr(), _nbytes(workspace),
+                               _stream_on(stream, dev)), "muon_qk_smax")
 
 
 def muon_test_gram_bf16(h, X, A, m, n, ldx, lda, s2=1.0, stream=None):

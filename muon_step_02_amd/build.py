@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
 
-SOURCES = ["api.hip", "plan.cpp", "elementwise.hip", "gemm_bf16.hip", "gemm_f32.hip"]
+SOURCES = ["api.hip", "plan.cpp", "elementwise.hip", "gemm_bf16.hip", "gemm_f32.hip",
+           "api_inputs.hip", "grads.hip", "experts.hip", "qk_smax.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

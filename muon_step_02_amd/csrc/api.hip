@@ -22,6 +22,7 @@
 #include <numeric>
 #include <vector>
 
+#include "context.h"
 #include "muon_internal.h"
 #include "plan.h"
 
@@ -32,26 +33,6 @@ namespace {
 constexpr float kMuonA = 3.4445f, kMuonB = -4.7750f, kMuonC = 2.0315f;
 
 }  // namespace
-
-struct TimedLaunch {
-    int phase;
-    hipEvent_t start, stop;
-};
-
-struct muon_context {
-    int device = 0;
-    float* scratch = nullptr;  // this device's copy of `scratch` (below), device address
-    int cus_per_xcd = 32;  // compute units per XCD (tile rounds)
-    // second stream (default priority) for the Newton-Schulz launches of the
-    // size classes other than the large one, forked from and joined back into
-    // the caller's stream with two events
-    hipStream_t side = nullptr;
-    hipEvent_t fork = nullptr, join = nullptr;
-    std::vector<char> table;  // host image of the descriptor table (reused)
-    bool profiling = false;
-    std::vector<TimedLaunch> timed;     // recorded since the last collect
-    std::vector<hipEvent_t> event_pool;  // timing events ready for reuse
-};
 
 // Device scratch of the allocation-free entry point adamw_step_clipped_noalloc:
 // the per-chunk partial sums of squares (one per kAdamwChunk elements) and,
@@ -83,59 +64,6 @@ hipError_t resolve_scratch(int device, float** out) {
     }
     *out = g_scratch_addr[device];
     return hipSuccess;
-}
-
-}  // namespace
-
-namespace {
-
-struct DeviceGuard {
-    int prev = -1;
-    bool changed = false;
-    explicit DeviceGuard(int dev) {
-        if (hipGetDevice(&prev) == hipSuccess && prev != dev) {
-            changed = hipSetDevice(dev) == hipSuccess;
-        }
-    }
-    ~DeviceGuard() {
-        if (changed) (void)hipSetDevice(prev);
-    }
-};
-
-inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
-
-bool finite(float v) { return isfinite(v) != 0; }
-
-size_t elem_bytes(int32_t dt) { return dt == MUON_BF16 ? 2 : 4; }
-bool valid_dtype(int32_t dt) { return dt == MUON_F32 || dt == MUON_BF16; }
-
-muon_status hip_status(hipError_t e) { return e == hipSuccess ? MUON_OK : MUON_ERR_HIP; }
-
-hipEvent_t take_event(muon_context* h) {
-    if (!h->event_pool.empty()) {
-        hipEvent_t e = h->event_pool.back();
-        h->event_pool.pop_back();
-        return e;
-    }
-    // timing only: no system-scope fence (its cache writeback would slow the
-    // launches being timed); the host reads nothing but the timestamps
-    hipEvent_t e = nullptr;
-    if (hipEventCreateWithFlags(&e, hipEventDisableSystemFence) != hipSuccess) return nullptr;
-    return e;
-}
-
-// Runs `launch` (a callable returning hipError_t); when profiling, brackets it
-// with two timing events on stream s.
-template <class F>
-hipError_t timed(muon_context* h, int phase, hipStream_t s, F&& launch) {
-    if (!h->profiling) return launch();
-    TimedLaunch t{phase, take_event(h), take_event(h)};
-    if (!t.start || !t.stop) return hipErrorOutOfMemory;
-    hipError_t e = hipEventRecord(t.start, s);
-    if (e == hipSuccess) e = launch();
-    if (e == hipSuccess) e = hipEventRecord(t.stop, s);
-    h->timed.push_back(t);
-    return e;
 }
 
 }  // namespace
@@ -211,9 +139,15 @@ muon_status muon_workspace_size(muon_handle h, const muon_matrix* mats, int n,
     return MUON_OK;
 }
 
-muon_status muon_step_batched(muon_handle h, const muon_matrix* mats, int n,
-                              const muon_hparams* hp, void* workspace, size_t workspace_bytes,
-                              void* stream) {
+}  // extern "C"
+
+namespace {
+
+// One Muon step; gscale: null, or the device scalar that multiplies every
+// gradient.
+muon_status step_batched(muon_handle h, const muon_matrix* mats, int n, const muon_hparams* hp,
+                         const float* gscale, void* workspace, size_t workspace_bytes,
+                         void* stream) {
     if (!h) return MUON_ERR_INVALID_ARG;
     const uintptr_t ws = reinterpret_cast<uintptr_t>(workspace);
     if (!workspace || ws % 256) return MUON_ERR_WORKSPACE;
@@ -246,7 +180,9 @@ muon_status muon_step_batched(muon_handle h, const muon_matrix* mats, int n,
         pc[c].upd = reinterpret_cast<const int32_t*>(ws + P.cls[c].off_pupd);
     }
 
-    hipError_t e = timed(h, 0, s, [&] { return launch_momentum(dd, n, eg, hp->momentum, hp->nesterov, s); });
+    hipError_t e = timed(h, 0, s, [&] {
+        return launch_momentum(dd, n, eg, hp->momentum, hp->nesterov, gscale, s);
+    });
     if (e == hipSuccess) e = timed(h, 1, s, [&] { return launch_norm_finalize(dd, n, hp->eps, s); });
     // The Newton-Schulz launches of different size classes read and write
     // disjoint buffers.  With more than one class in use, every class but the
@@ -333,6 +269,28 @@ muon_status muon_step_batched(muon_handle h, const muon_matrix* mats, int n,
             return launch_apply(dd, n, eg, hp->ns_steps & 1, hp->lr, hp->weight_decay, hp->qk_tau, s);
         });
     return hip_status(e);
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status muon_step_batched(muon_handle h, const muon_matrix* mats, int n,
+                              const muon_hparams* hp, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    return step_batched(h, mats, n, hp, nullptr, workspace, workspace_bytes, stream);
+}
+
+muon_status muon_step_batched_scaled(muon_handle h, const muon_matrix* mats, int n,
+                                     const muon_hparams* hp, const float* grad_scale,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+    if (!grad_scale) return MUON_ERR_INVALID_ARG;
+    const uintptr_t gs = reinterpret_cast<uintptr_t>(grad_scale);
+    const uintptr_t ws = reinterpret_cast<uintptr_t>(workspace);
+    if (gs % 4) return MUON_ERR_UNALIGNED;
+    // the step writes its workspace before it reads the scale
+    if (gs >= ws && gs - ws < workspace_bytes) return MUON_ERR_OVERLAP;
+    return step_batched(h, mats, n, hp, grad_scale, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"
@@ -435,6 +393,16 @@ muon_status adamw_step(muon_handle h, const adamw_tensor* ts, int n, const adamw
     if (st != MUON_OK) return st;
     DeviceGuard g(h->device);
     return hip_status(adamw_launch_all(h, ts, n, hp, nullptr, reinterpret_cast<hipStream_t>(stream)));
+}
+
+muon_status adamw_step_scaled(muon_handle h, const adamw_tensor* ts, int n, const adamw_hparams* hp,
+                              const float* grad_scale, void* stream) {
+    if (!h || !grad_scale) return MUON_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(grad_scale) % 4) return MUON_ERR_UNALIGNED;
+    muon_status st = check_adamw(ts, n, hp);
+    if (st != MUON_OK) return st;
+    DeviceGuard g(h->device);
+    return hip_status(adamw_launch_all(h, ts, n, hp, grad_scale, reinterpret_cast<hipStream_t>(stream)));
 }
 
 muon_status adamw_workspace_size(muon_handle h, const adamw_tensor* ts, int n, size_t* bytes) {

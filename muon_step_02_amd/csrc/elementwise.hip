@@ -179,9 +179,12 @@ struct EwTile {
 // both the column writes and the row reads on distinct banks).
 constexpr int lds_tile(int th, int tw) { return tw * (th + 1); }
 
-template <bool VEC, bool NS_F32, int TH, int TW, bool GBF>
+// SCALED: every gradient element is multiplied by gs first (global-norm
+// clipping).  A variant of its own, so that the unscaled step stays the same
+// arithmetic, contraction of its products into fused ones included.
+template <bool VEC, bool NS_F32, int TH, int TW, bool GBF, bool SCALED>
 __device__ __forceinline__ void momentum_tile(const MatDesc& d, int lt, float mu, int nesterov,
-                                              float* tileT, float* red) {
+                                              float gs, float* tileT, float* red) {
     using T = EwTile<TH, TW>;
     constexpr bool TRN = TH != 16;  // the tile goes through LDS
     const int tr = lt / d.ew_tiles_c, tc = lt - tr * d.ew_tiles_c;
@@ -221,6 +224,10 @@ __device__ __forceinline__ void momentum_tile(const MatDesc& d, int lt, float mu
         const int64_t c = c0 + cg;
         float y[4] = {0.f, 0.f, 0.f, 0.f};
         if (valid[q] > 0) {
+            if constexpr (SCALED) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) g[q].v[e] *= gs;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float mn = mu * m[q].v[e] + omm * g[q].v[e];
@@ -257,16 +264,16 @@ __device__ __forceinline__ void momentum_tile(const MatDesc& d, int lt, float mu
 // The dtype and alignment of a matrix are uniform over the workgroup: branch
 // once here, so the tile's loads are straight-line code that can all be in
 // flight together.
-template <bool NS_F32, int TH, int TW>
+template <bool NS_F32, int TH, int TW, bool SCALED>
 __device__ __forceinline__ void momentum_dispatch(const MatDesc& d, int lt, float mu, int nesterov,
-                                                  float* tileT, float* red) {
+                                                  float gs, float* tileT, float* red) {
     const bool gbf = d.grad_dtype == MUON_BF16;
     if (d.vec4) {
-        if (gbf) momentum_tile<true, NS_F32, TH, TW, true>(d, lt, mu, nesterov, tileT, red);
-        else momentum_tile<true, NS_F32, TH, TW, false>(d, lt, mu, nesterov, tileT, red);
+        if (gbf) momentum_tile<true, NS_F32, TH, TW, true, SCALED>(d, lt, mu, nesterov, gs, tileT, red);
+        else momentum_tile<true, NS_F32, TH, TW, false, SCALED>(d, lt, mu, nesterov, gs, tileT, red);
     } else {
-        if (gbf) momentum_tile<false, NS_F32, TH, TW, true>(d, lt, mu, nesterov, tileT, red);
-        else momentum_tile<false, NS_F32, TH, TW, false>(d, lt, mu, nesterov, tileT, red);
+        if (gbf) momentum_tile<false, NS_F32, TH, TW, true, SCALED>(d, lt, mu, nesterov, gs, tileT, red);
+        else momentum_tile<false, NS_F32, TH, TW, false, SCALED>(d, lt, mu, nesterov, gs, tileT, red);
     }
 }
 
@@ -276,22 +283,23 @@ constexpr int ew_lds_floats() {
     return !LDS ? 1 : NS_F32 ? lds_tile(kEwTile, kEwTile) : lds_tile(kTrTH, kTrTW);
 }
 
-template <bool NS_F32, bool LDS>
+template <bool NS_F32, bool LDS, bool SCALED>
 __global__ __launch_bounds__(256) void momentum_kernel(const MatDesc* __restrict__ descs, int n,
                                                        const int32_t* __restrict__ prefix,
-                                                       float mu, int nesterov) {
+                                                       float mu, int nesterov, const float* gscale) {
     __shared__ float tileT[ew_lds_floats<NS_F32, LDS>()];
     __shared__ float red[4];
     const int tile = blockIdx.x;
     const int mi = find_matrix(prefix, n, tile);
     const MatDesc& d = descs[mi];
     const int lt = tile - prefix[mi];
+    const float gs = SCALED ? gld(gscale) : 1.f;
     if (NS_F32)
-        momentum_dispatch<true, kEwTile, kEwTile>(d, lt, mu, nesterov, tileT, red);
+        momentum_dispatch<true, kEwTile, kEwTile, SCALED>(d, lt, mu, nesterov, gs, tileT, red);
     else if (!LDS)
-        momentum_dispatch<false, 16, 256>(d, lt, mu, nesterov, tileT, red);
+        momentum_dispatch<false, 16, 256, SCALED>(d, lt, mu, nesterov, gs, tileT, red);
     else
-        momentum_dispatch<false, kTrTH, kTrTW>(d, lt, mu, nesterov, tileT, red);
+        momentum_dispatch<false, kTrTH, kTrTW, SCALED>(d, lt, mu, nesterov, gs, tileT, red);
 }
 
 __global__ __launch_bounds__(256) void norm_finalize_kernel(const MatDesc* __restrict__ descs,
@@ -606,14 +614,28 @@ hipError_t launch_clip_finalize(const float* partials, int nblocks, float max_no
     return hipGetLastError();
 }
 
-hipError_t launch_momentum(const MatDesc* d, int n, const EwGroups& g, float mu, int nesterov,
-                           hipStream_t st) {
+namespace {
+template <bool SCALED>
+void momentum_launches(const MatDesc* d, int n, const EwGroups& g, float mu, int nesterov,
+                       const float* gscale, hipStream_t st) {
     if (g.tiles[kEwStream] > 0)
-        momentum_kernel<false, false><<<g.tiles[kEwStream], 256, 0, st>>>(d, n, g.prefix[kEwStream], mu, nesterov);
+        momentum_kernel<false, false, SCALED><<<g.tiles[kEwStream], 256, 0, st>>>(
+            d, n, g.prefix[kEwStream], mu, nesterov, gscale);
     if (g.tiles[kEwTrans] > 0)
-        momentum_kernel<false, true><<<g.tiles[kEwTrans], 256, 0, st>>>(d, n, g.prefix[kEwTrans], mu, nesterov);
+        momentum_kernel<false, true, SCALED><<<g.tiles[kEwTrans], 256, 0, st>>>(
+            d, n, g.prefix[kEwTrans], mu, nesterov, gscale);
     if (g.tiles[kEwF32] > 0)
-        momentum_kernel<true, true><<<g.tiles[kEwF32], 256, 0, st>>>(d, n, g.prefix[kEwF32], mu, nesterov);
+        momentum_kernel<true, true, SCALED><<<g.tiles[kEwF32], 256, 0, st>>>(
+            d, n, g.prefix[kEwF32], mu, nesterov, gscale);
+}
+}  // namespace
+
+hipError_t launch_momentum(const MatDesc* d, int n, const EwGroups& g, float mu, int nesterov,
+                           const float* gscale, hipStream_t st) {
+    if (gscale)
+        momentum_launches<true>(d, n, g, mu, nesterov, gscale, st);
+    else
+        momentum_launches<false>(d, n, g, mu, nesterov, nullptr, st);
     return hipGetLastError();
 }
 

@@ -1,0 +1,332 @@
+// Global gradient norm over many tensors, and the clip to it (gfx950).
+//
+//   norm  = sqrt(sum over tensors and elements of g^2)
+//   scale = max_norm / norm where norm > max_norm, else 1
+//   out   = g * scale
+//
+// ("Por qué AdamW para entrenar modelos de lenguaje, y qué está cambiando",
+// gustavoai.dev, section "Por qué AdamW, y por qué con esos números": before
+// g enters the moments, a norm above 1 is rescaled to 1.)
+//
+// Both passes are bound by HBM: the norm reads every gradient once, the clip
+// reads it again and writes the output.  Squares are formed and added up in
+// 64 bits: the fp64 rate leaves room (one conversion and one fused
+// multiply-add per element, a fifth of what the vector units do in the time
+// the loads take), and no gradient that fp32 can hold overflows or vanishes
+// in its square.  Every sum has a fixed order, so results are bitwise
+// repeatable: block b takes chunks b, b + blocks, ... of the group.
+#include "inputs.h"
+
+namespace muon {
+
+namespace {
+
+// 16 bytes at the alignment of an element: rows of any leading dimension are
+// read with full-width loads (gfx950 allows unaligned global accesses).
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
+typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+
+constexpr int kQ = kGradUnits / 256;  // units per thread and chunk
+
+template <bool BF>
+struct Elems {
+    static constexpr int V = BF ? 8 : 4;  // elements of a unit
+    float v[V];
+};
+
+// The unit at element offset `off`; `left`: elements the row still holds.
+template <bool BF>
+__device__ __forceinline__ Elems<BF> load_unit(const void* base, int64_t off, int64_t left) {
+    Elems<BF> r;
+    constexpr int V = Elems<BF>::V;
+    if (left >= V) {
+        if constexpr (BF) {
+            const u16x8u u = *(const MUON_GLOBAL u16x8u*)(reinterpret_cast<const uint16_t*>(base) + off);
+#pragma unroll
+            for (int e = 0; e < V; ++e) r.v[e] = bf16_bits_to_f32(u[e]);
+        } else {
+            const f32x4u u = *(const MUON_GLOBAL f32x4u*)(reinterpret_cast<const float*>(base) + off);
+#pragma unroll
+            for (int e = 0; e < V; ++e) r.v[e] = u[e];
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            r.v[e] = 0.f;
+            if (e < left)
+                r.v[e] = BF ? bf16_bits_to_f32(gld(reinterpret_cast<const uint16_t*>(base) + off + e))
+                            : gld(reinterpret_cast<const float*>(base) + off + e);
+        }
+    }
+    return r;
+}
+
+template <int V, bool OBF>
+__device__ __forceinline__ void store_unit(void* base, int64_t off, int64_t left, const float* v) {
+    if (left >= V) {
+#pragma unroll
+        for (int h = 0; h < V / 4; ++h) {
+            if constexpr (OBF) {
+                u16x4u o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = f32_to_bf16_bits(v[4 * h + e]);
+                *(MUON_GLOBAL u16x4u*)(reinterpret_cast<uint16_t*>(base) + off + 4 * h) = o;
+            } else {
+                f32x4u o;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[e] = v[4 * h + e];
+                *(MUON_GLOBAL f32x4u*)(reinterpret_cast<float*>(base) + off + 4 * h) = o;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (e < left) {
+                if (OBF)
+                    gst(reinterpret_cast<uint16_t*>(base) + off + e, f32_to_bf16_bits(v[e]));
+                else
+                    gst(reinterpret_cast<float*>(base) + off + e, v[e]);
+            }
+        }
+    }
+}
+
+template <int CAP>
+__device__ __forceinline__ int grad_tensor_of(const GradGroup<CAP>& grp, int chunk) {
+    int lo = 0, hi = grp.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (grp.chunk_prefix[mid] <= chunk) lo = mid; else hi = mid - 1;
+    }
+    return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// Where a thread's units of a chunk lie: unit u of the tensor is row u / upr,
+// elements (u % upr) * V ... of that row (upr units a row).  One division for
+// the first unit; the others are 256 units further on each.
+struct Walk {
+    int64_t r, c;       // row, unit within the row
+    int64_t dr, dc;     // 256 units further
+    int64_t upr, rows;
+    __device__ __forceinline__ Walk(int64_t u, int64_t upr_, int64_t rows_) : upr(upr_), rows(rows_) {
+        if (rows == 1) {
+            r = 0;
+            c = u;
+            dr = 0;
+            dc = 256;
+        } else if (upr <= 0xffffffffll && u <= 0xffffffffll) {
+            r = (uint32_t)u / (uint32_t)upr;
+            c = u - r * upr;
+            dr = 256u / (uint32_t)upr;
+            dc = 256 - dr * upr;
+        } else {
+            r = u / upr;
+            c = u - r * upr;
+            dr = 256 / upr;
+            dc = 256 - dr * upr;
+        }
+    }
+    __device__ __forceinline__ bool inside() const { return r < rows && c < upr; }
+    __device__ __forceinline__ void next() {
+        r += dr;
+        c += dc;
+        if (rows > 1 && c >= upr) {
+            c -= upr;
+            ++r;
+        }
+    }
+};
+
+template <bool BF>
+__device__ __forceinline__ void chunk_sumsq(const void* g, int64_t rows, int64_t cols, int64_t ld,
+                                            int64_t first, double (&acc)[4]) {
+    constexpr int V = Elems<BF>::V;
+    Walk w(first + threadIdx.x, (cols + V - 1) / V, rows);
+    Elems<BF> x[kQ];
+    // every load first, so that all are in flight together
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        x[q] = load_unit<BF>(g, w.r * ld + w.c * V, w.inside() ? cols - w.c * V : 0);
+        w.next();
+    }
+#pragma unroll
+    for (int q = 0; q < kQ; ++q)
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const double d = (double)x[q].v[e];
+            acc[e & 3] = fma(d, d, acc[e & 3]);
+        }
+}
+
+template <bool BF, bool OBF>
+__device__ __forceinline__ void chunk_scale(const void* g, void* out, int64_t rows, int64_t cols,
+                                            int64_t ld, int64_t ld_out, int64_t first, float scale) {
+    constexpr int V = Elems<BF>::V;
+    const Walk w0(first + threadIdx.x, (cols + V - 1) / V, rows);
+    Elems<BF> x[kQ];
+    Walk w = w0;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+        x[q] = load_unit<BF>(g, w.r * ld + w.c * V, w.inside() ? cols - w.c * V : 0);
+        w.next();
+    }
+    w = w0;
+#pragma unroll
+    for (int q = 0; q < kQ; ++q) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) x[q].v[e] *= scale;
+        store_unit<V, OBF>(out, w.r * ld_out + w.c * V, w.inside() ? cols - w.c * V : 0, x[q].v);
+        w.next();
+    }
+}
+
+template <int CAP>
+__device__ __forceinline__ void group_sumsq(const GradGroup<CAP>& grp, int b, int blocks, double (&acc)[4]) {
+    const int chunks = grp.chunk_prefix[grp.count];
+    for (int ch = b; ch < chunks; ch += blocks) {
+        const int t = grad_tensor_of(grp, ch);
+        const int64_t first = (int64_t)(ch - grp.chunk_prefix[t]) * kGradUnits;
+        if (grp.bf16[t])
+            chunk_sumsq<true>(grp.g[t], grp.rows[t], grp.cols[t], grp.ld_g[t], first, acc);
+        else
+            chunk_sumsq<false>(grp.g[t], grp.rows[t], grp.cols[t], grp.ld_g[t], first, acc);
+    }
+}
+
+// The chunks in the order opposite to the sum's: what it read last is the
+// likeliest to be left in the memory-side cache.
+template <int CAP>
+__device__ __forceinline__ void group_scale(const GradGroup<CAP>& grp, int b, int blocks, float scale) {
+    const int chunks = grp.chunk_prefix[grp.count];
+    for (int k = b; k < chunks; k += blocks) {
+        const int ch = chunks - 1 - k;
+        const int t = grad_tensor_of(grp, ch);
+        // nothing to do in place where nothing is clipped
+        if (scale == 1.f && grp.out[t] == grp.g[t]) continue;
+        const int64_t first = (int64_t)(ch - grp.chunk_prefix[t]) * kGradUnits;
+        const int64_t rows = grp.rows[t], cols = grp.cols[t], lg = grp.ld_g[t], lo = grp.ld_out[t];
+        if (grp.bf16[t]) {
+            if (grp.out_bf16[t])
+                chunk_scale<true, true>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
+            else
+                chunk_scale<true, false>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
+        } else {
+            if (grp.out_bf16[t])
+                chunk_scale<false, true>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
+            else
+                chunk_scale<false, false>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
+        }
+    }
+}
+
+// Sum over the workgroup, the same value in every thread, in a fixed order.
+template <int NT>
+__device__ __forceinline__ double block_sum(double s, double* red) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) s += __shfl_xor(s, off, 64);
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = s;
+    __syncthreads();
+    double t = red[0];
+#pragma unroll
+    for (int w = 1; w < NT / 64; ++w) t += red[w];
+    return t;
+}
+
+__device__ __forceinline__ float clip_scale(double sumsq, float max_norm, float* norm_out,
+                                            float* scale_out, bool write) {
+    const double norm = sqrt(sumsq);
+    const float scale = norm > (double)max_norm ? (float)((double)max_norm / norm) : 1.f;
+    if (write) {
+        if (norm_out) gst(norm_out, (float)norm);
+        if (scale_out) gst(scale_out, scale);
+    }
+    return scale;
+}
+
+template <int NT>
+__device__ __forceinline__ double partials_sum(const double* partials, int n, double* red) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n; i += NT) s += gld(partials + i);
+    return block_sum<NT>(s, red);
+}
+
+template <int CAP>
+__global__ __launch_bounds__(256) void grad_sumsq_kernel(GradGroup<CAP> grp, int blocks,
+                                                         double* partials) {
+    __shared__ double red[4];
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    group_sumsq(grp, blockIdx.x, blocks, acc);
+    const double tot = block_sum<256>((acc[0] + acc[1]) + (acc[2] + acc[3]), red);
+    if (threadIdx.x == 0) gst(partials + blockIdx.x, tot);
+}
+
+__global__ __launch_bounds__(256) void grad_finalize_kernel(const double* partials, int n,
+                                                            float max_norm, float* norm_out,
+                                                            float* scale_out) {
+    __shared__ double red[4];
+    const double s = partials_sum<256>(partials, n, red);
+    clip_scale(s, max_norm, norm_out, scale_out, threadIdx.x == 0);
+}
+
+template <int CAP>
+__global__ __launch_bounds__(256) void grad_scale_kernel(GradGroup<CAP> grp, int blocks,
+                                                         const double* partials, int n,
+                                                         float max_norm, float* norm_out,
+                                                         float* scale_out) {
+    __shared__ double red[4];
+    const double s = partials_sum<256>(partials, n, red);
+    const float scale = clip_scale(s, max_norm, norm_out, scale_out, blockIdx.x == 0 && threadIdx.x == 0);
+    group_scale(grp, blockIdx.x, blocks, scale);
+}
+
+template <int CAP>
+__global__ __launch_bounds__(256) void grad_single_kernel(GradGroup<CAP> grp, int clip, float max_norm,
+                                                          float* norm_out, float* scale_out) {
+    __shared__ double red[4];
+    double acc[4] = {0.0, 0.0, 0.0, 0.0};
+    group_sumsq(grp, 0, 1, acc);
+    // the barrier within also keeps the outputs behind every read of the sum
+    const double s = block_sum<256>((acc[0] + acc[1]) + (acc[2] + acc[3]), red);
+    const float scale = clip_scale(s, max_norm, norm_out, scale_out, threadIdx.x == 0);
+    if (clip) group_scale(grp, 0, 1, scale);
+}
+
+}  // namespace
+
+template <int CAP>
+hipError_t launch_grad_sumsq(const GradGroup<CAP>& g, int blocks, double* partials, hipStream_t st) {
+    grad_sumsq_kernel<CAP><<<blocks, 256, 0, st>>>(g, blocks, partials);
+    return hipGetLastError();
+}
+
+hipError_t launch_grad_finalize(const double* partials, int nparts, float max_norm, float* norm_out,
+                                float* scale_out, hipStream_t st) {
+    grad_finalize_kernel<<<1, 256, 0, st>>>(partials, nparts, max_norm, norm_out, scale_out);
+    return hipGetLastError();
+}
+
+template <int CAP>
+hipError_t launch_grad_scale(const GradGroup<CAP>& g, int blocks, const double* partials, int nparts,
+                             float max_norm, float* norm_out, float* scale_out, hipStream_t st) {
+    grad_scale_kernel<CAP><<<blocks, 256, 0, st>>>(g, blocks, partials, nparts, max_norm, norm_out, scale_out);
+    return hipGetLastError();
+}
+
+template <int CAP>
+hipError_t launch_grad_single(const GradGroup<CAP>& g, int clip, float max_norm, float* norm_out,
+                              float* scale_out, hipStream_t st) {
+    grad_single_kernel<CAP><<<1, 256, 0, st>>>(g, clip, max_norm, norm_out, scale_out);
+    return hipGetLastError();
+}
+
+#define MUON_GRAD_GROUPS(CAP)                                                                        \
+    template hipError_t launch_grad_sumsq<CAP>(const GradGroup<CAP>&, int, double*, hipStream_t);    \
+    template hipError_t launch_grad_scale<CAP>(const GradGroup<CAP>&, int, const double*, int, float, \
+                                               float*, float*, hipStream_t);                         \
+    template hipError_t launch_grad_single<CAP>(const GradGroup<CAP>&, int, float, float*, float*,   \
+                                                hipStream_t);
+MUON_GRAD_GROUPS(kGradGroupSmall)
+MUON_GRAD_GROUPS(kGradGroup)
+
+}  // namespace muon

@@ -71,8 +71,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 // the MI355X: a 2 KB argument block takes 3.4 us a launch, 16 KB 7.5 us.
 constexpr int kTableChunkWords = 4096;
 hipError_t launch_table_upload(const void* host, size_t bytes, void* dst, hipStream_t st);
+// gscale: null, or a device scalar every gradient is multiplied by first
 hipError_t launch_momentum(const MatDesc* d, int n, const EwGroups& g, float mu, int nesterov,
-                           hipStream_t st);
+                           const float* gscale, hipStream_t st);
 hipError_t launch_norm_finalize(const MatDesc* d, int n, float eps, hipStream_t st);
 hipError_t launch_apply(const MatDesc* d, int n, const EwGroups& g, int final_parity, float lr,
                         float wd, float qk_tau, hipStream_t st);

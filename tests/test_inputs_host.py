@@ -1,0 +1,280 @@
+"""Operators on the step's inputs (gradient norm and clip, expert products,
+largest attention logits): what their entry points refuse, and the layout of
+their structures.  No GPU: every refusal comes before a call touches a
+device, so a zeroed block of memory stands in for the handle."""
+
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+import muon_step_02_amd as mu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+INVALID, WORKSPACE, OVERLAP, UNALIGNED = 1, 3, 4, 6
+BUF = 1 << 20  # an address for tensors that no call gets to read
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return mu.load()
+
+
+@pytest.fixture(scope="module")
+def handle():
+    return ctypes.cast(ctypes.create_string_buffer(4096), ctypes.c_void_p)
+
+
+def test_structures_match_the_header(tmp_path):
+    structs = {"muon_grad": mu.MuonGrad, "muon_experts": mu.MuonExperts, "muon_qk": mu.MuonQk}
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "muon.h"', "int main(void){"]
+    for name, cls in structs.items():
+        lines.append('printf("%s %%zu\\n", sizeof(%s));' % (name, name))
+        lines += ['printf("%s.%s %%zu\\n", offsetof(%s, %s));' % (name, f, name, f)
+                  for f, _ in cls._fields_]
+    c, exe = tmp_path / "s.c", tmp_path / "s"
+    c.write_text("\n".join(lines + ["return 0;}"]))
+    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(c), "-o", str(exe)],
+                   check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    got = {k: int(v) for k, v in (line.split() for line in out.splitlines())}
+    for name, cls in structs.items():
+        assert got[name] == ctypes.sizeof(cls)
+        for f, _ in cls._fields_:
+            assert got["%s.%s" % (name, f)] == getattr(cls, f).offset, (name, f)
+
+
+# ---- gradient norm and clip ------------------------------------------------
+
+def _grad(**over):
+    d = dict(grad=BUF, out=BUF, rows=4, cols=8, ld_grad=8, ld_out=8, grad_dtype=0, out_dtype=0)
+    d.update(over)
+    return mu.MuonGrad(**d)
+
+
+def _grad_call(lib, h, grads, clip=True, max_norm=1.0, norm=4 * BUF, scale=None, ws=8 * BUF,
+               nbytes=1 << 20):
+    arr = (mu.MuonGrad * max(len(grads), 1))(*grads)
+    fn = lib.muon_grad_clip if clip else lib.muon_grad_norm
+    return fn(h, arr, len(grads), max_norm, norm, scale, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("clip", [False, True])
+@pytest.mark.parametrize("over", [dict(rows=-1), dict(cols=-1), dict(ld_grad=7), dict(grad_dtype=2),
+                                  dict(grad=None), dict(rows=1 << 41), dict(cols=1 << 41),
+                                  dict(rows=1 << 39, cols=1 << 39, ld_grad=1 << 39)])
+def test_grad_sizes_refused(lib, handle, clip, over):
+    assert _grad_call(lib, handle, [_grad(**over)], clip) == INVALID
+
+
+@pytest.mark.parametrize("over", [dict(out=None), dict(out_dtype=5), dict(ld_out=7)])
+def test_grad_outputs_refused(lib, handle, over):
+    assert _grad_call(lib, handle, [_grad(**over)]) == INVALID
+
+
+@pytest.mark.parametrize("clip", [False, True])
+def test_grad_arguments_refused(lib, handle, clip):
+    g = [_grad()]
+    assert _grad_call(lib, handle, [], clip) == INVALID
+    assert _grad_call(lib, None, g, clip) == INVALID
+    for bad in (0.0, -1.0, float("inf"), float("nan")):
+        assert _grad_call(lib, handle, g, clip, max_norm=bad) == INVALID
+    assert _grad_call(lib, handle, g, clip, ws=None) == WORKSPACE
+    assert _grad_call(lib, handle, g, clip, ws=8 * BUF + 128) == WORKSPACE
+    assert _grad_call(lib, handle, g, clip, nbytes=64) == WORKSPACE
+    assert _grad_call(lib, handle, g, clip, norm=BUF + 2) == UNALIGNED
+    assert _grad_call(lib, handle, [_grad(grad=BUF + 2, out=BUF + 2)], clip) == UNALIGNED
+    if not clip:
+        assert _grad_call(lib, handle, g, False, norm=None, scale=None) == INVALID
+
+
+def test_clip_outputs_that_share_memory_are_refused(lib, handle):
+    def both(a, b):
+        return _grad_call(lib, handle, [a, b], nbytes=0)  # refused for its workspace, if at all
+
+    far = _grad(grad=2 * BUF, out=2 * BUF)
+    assert both(_grad(), far) == WORKSPACE
+    assert both(_grad(), _grad()) == OVERLAP                              # one tensor twice
+    assert both(_grad(), _grad(grad=2 * BUF, out=BUF + 64)) == OVERLAP    # into another's gradient
+    assert both(_grad(out=3 * BUF), _grad(grad=2 * BUF, out=3 * BUF)) == OVERLAP
+    assert both(_grad(out=3 * BUF), _grad(out=4 * BUF)) == WORKSPACE      # one gradient read twice
+    # its own gradient, but not exactly in place
+    assert both(_grad(out=BUF + 32), far) == OVERLAP
+    assert both(_grad(grad_dtype=1), far) == OVERLAP
+    assert both(_grad(ld_out=16), far) == OVERLAP
+    # column blocks of one buffer interleave without sharing
+    left, right = (_grad(grad=BUF + o, out=BUF + o, ld_grad=16, ld_out=16) for o in (0, 32))
+    assert both(left, right) == WORKSPACE
+    assert both(left, _grad(grad=BUF + 28, out=BUF + 28, ld_grad=16, ld_out=16)) == OVERLAP
+    assert both(left, _grad(grad=BUF + 36, out=BUF + 36, ld_grad=16, ld_out=16)) == OVERLAP
+
+
+def test_grad_workspace_size(lib, handle):
+    for n in (1, 16, 17, 257, 5000):
+        sz = ctypes.c_size_t()
+        arr = (mu.MuonGrad * n)(*[_grad()] * n)
+        assert lib.muon_grad_workspace_size(handle, arr, n, ctypes.byref(sz)) == 0
+        assert sz.value % 256 == 0 and sz.value >= 8 * 2048
+    assert lib.muon_grad_workspace_size(handle, arr, 0, ctypes.byref(sz)) == INVALID
+
+
+def test_scaled_steps_need_a_scale(lib, handle):
+    mats, hp = (mu.MuonMatrix * 1)(), mu.muon_hparams(lr=1e-3)
+    assert lib.muon_step_batched_scaled(handle, mats, 1, ctypes.byref(hp), None, BUF, 1 << 20, None) == INVALID
+    assert lib.muon_step_batched_scaled(handle, mats, 1, ctypes.byref(hp), BUF + 1, BUF, 1 << 20, None) == UNALIGNED
+    ts, ahp = (mu.AdamwTensor * 1)(), mu.adamw_hparams(1e-3, 1)
+    assert lib.adamw_step_scaled(handle, ts, 1, ctypes.byref(ahp), None, None) == INVALID
+    assert lib.adamw_step_scaled(handle, ts, 1, ctypes.byref(ahp), BUF + 2, None) == UNALIGNED
+    m = mu.MuonMatrix(param=2 * BUF, grad=3 * BUF, momentum=4 * BUF, rows=64, cols=64, ld_param=64,
+                      ld_grad=64, ld_mom=64)
+    mats = (mu.MuonMatrix * 1)(m)
+    assert lib.muon_step_batched_scaled(handle, mats, 1, ctypes.byref(hp), 8 * BUF + 4, 8 * BUF,
+                                        1 << 30, None) == OVERLAP
+
+
+def test_grad_descriptors():
+    t = torch.zeros(6, 10)
+    g = mu.muon_grad(t[:, 2:7])
+    assert (g.rows, g.cols, g.ld_grad, g.grad, g.out) == (6, 5, 10, t.data_ptr() + 8, None)
+    g = mu.muon_grad(t.view(3, 2, 10))
+    assert (g.rows, g.cols, g.ld_grad) == (1, 60, 60)
+    g = mu.muon_grad(torch.zeros(5, dtype=torch.bfloat16), torch.zeros(5))
+    assert (g.rows, g.cols, g.grad_dtype, g.out_dtype) == (1, 5, 1, 0)
+    g = mu.muon_grad(torch.zeros(()))
+    assert (g.rows, g.cols) == (1, 1)
+    g = mu.muon_grad(torch.zeros(0, 7))
+    assert g.rows * g.cols == 0
+    for bad in (t.t(), t[:, ::2], t[:1].expand(6, 10), t.view(3, 2, 10)[:, :, :4]):
+        with pytest.raises(ValueError):
+            mu.muon_grad(bad)
+    with pytest.raises(ValueError):
+        mu.muon_grad(t, torch.zeros(10, 6))
+    with pytest.raises(TypeError):
+        mu.muon_grad(t.half())
+
+
+# ---- expert products ---------------------------------------------------------
+
+def _experts(n=3, at=BUF, step=1 << 14, **over):
+    ptrs = (ctypes.c_void_p * max(n, 1))(*[at + i * step for i in range(n)])
+    d = dict(weights=ptrs, rows=16, cols=32, ld=32, experts=n, dtype=1)
+    d.update(over)
+    ex = mu.MuonExperts(**d)
+    ex._keep = ptrs
+    return ex
+
+
+def _rows_call(lib, h, ex, name="muon_expert_forward", offsets=9 * BUF, x=4 * BUF, ld_x=32, y=6 * BUF,
+               ld_y=32, tokens=10):
+    return getattr(lib, name)(h, ctypes.byref(ex), offsets, x, ld_x, y, ld_y, tokens, None)
+
+
+def _weight_call(lib, h, ex, offsets=9 * BUF, x=4 * BUF, ld_x=32, dy=6 * BUF, ld_dy=16, tokens=10,
+                 dtype=1, accumulate=0):
+    return lib.muon_expert_grad_weight(h, ctypes.byref(ex), offsets, x, ld_x, dy, ld_dy, tokens, dtype,
+                                       accumulate, None)
+
+
+@pytest.mark.parametrize("over", [dict(experts=0), dict(experts=1025), dict(rows=0), dict(cols=0),
+                                  dict(ld=31), dict(dtype=2), dict(rows=(1 << 20) + 1),
+                                  dict(weights=None)])
+def test_experts_refused(lib, handle, over):
+    ex = _experts(**over)
+    for name in ("muon_expert_forward", "muon_expert_grad_input"):
+        assert _rows_call(lib, handle, ex, name) == INVALID
+    assert _weight_call(lib, handle, ex) == INVALID
+
+
+def test_expert_pointers_refused(lib, handle):
+    ex = _experts()
+    ex.weights[1] = None
+    assert _rows_call(lib, handle, ex) == INVALID and _weight_call(lib, handle, ex) == INVALID
+    ex = _experts(at=BUF + 1)
+    assert _rows_call(lib, handle, ex) == UNALIGNED and _weight_call(lib, handle, ex) == UNALIGNED
+
+
+@pytest.mark.parametrize("over,status", [
+    (dict(offsets=None), INVALID), (dict(offsets=9 * BUF + 2), UNALIGNED), (dict(x=None), INVALID),
+    (dict(ld_x=15), INVALID), (dict(tokens=-1), INVALID), (dict(tokens=1 << 31), INVALID),
+    (dict(x=4 * BUF + 1), UNALIGNED)])
+def test_expert_tokens_refused(lib, handle, over, status):
+    ex = _experts()
+    assert _rows_call(lib, handle, ex, **over) == status
+    assert _weight_call(lib, handle, ex, **over) == status
+
+
+def test_expert_outputs_refused(lib, handle):
+    ex = _experts()
+    assert _rows_call(lib, handle, ex, y=None) == INVALID
+    assert _rows_call(lib, handle, ex, ld_y=15) == INVALID
+    assert _rows_call(lib, handle, ex, "muon_expert_grad_input", ld_y=31) == INVALID
+    assert _rows_call(lib, handle, ex, y=4 * BUF + 64) == OVERLAP      # onto x
+    assert _rows_call(lib, handle, ex, y=BUF + 512) == OVERLAP         # onto a weight
+    assert _rows_call(lib, handle, ex, y=9 * BUF - 64) == OVERLAP      # onto the offsets
+    assert _rows_call(lib, None, ex) == INVALID
+    assert _rows_call(lib, handle, ex, tokens=0, x=None, y=None) == 0  # nothing to do
+
+
+def test_expert_weight_gradients_refused(lib, handle):
+    assert _weight_call(lib, handle, _experts(step=0)) == OVERLAP      # one gradient for two experts
+    assert _weight_call(lib, handle, _experts(step=64)) == OVERLAP
+    assert _weight_call(lib, handle, _experts(), x=BUF + 512) == OVERLAP
+    assert _weight_call(lib, handle, _experts(), dy=BUF + 512) == OVERLAP
+    assert _weight_call(lib, handle, _experts(), accumulate=2) == INVALID
+    assert _weight_call(lib, handle, _experts(), dtype=3) == INVALID
+    assert _weight_call(lib, handle, _experts(), dtype=0) == INVALID   # fp32 tokens, bf16 gradients
+    assert _weight_call(lib, handle, _experts(rows=1 << 20, cols=1 << 20, ld=1 << 20, n=1024),
+                        ld_x=1 << 20, ld_dy=1 << 20) == INVALID        # more tiles than a launch holds
+
+
+def test_expert_binding_refuses(monkeypatch):
+    cpu = torch.zeros(4, 8)
+    with pytest.raises(ValueError):
+        mu.muon_experts([cpu])      # not on a GPU
+    with pytest.raises(ValueError):
+        mu.muon_experts([])
+
+
+# ---- largest attention logits -------------------------------------------------
+
+def _qk(**over):
+    d = dict(q=BUF, k=2 * BUF, tokens_q=10, tokens_k=12, q_token=128, q_head=32, k_token=64, k_head=32,
+             cu_q=3 * BUF, cu_k=3 * BUF + 64, sequences=2, heads_q=4, heads_k=2, head_dim=32, dtype=1,
+             causal=1, scale=0.5)
+    d.update(over)
+    return mu.MuonQk(**d)
+
+
+def _smax_call(lib, h, qk, q=4 * BUF, k=5 * BUF, accumulate=0, ws=6 * BUF, nbytes=1 << 20):
+    return lib.muon_qk_smax(h, ctypes.byref(qk), q, k, accumulate, ws, nbytes, None)
+
+
+@pytest.mark.parametrize("over", [
+    dict(heads_q=0), dict(heads_k=0), dict(heads_q=3), dict(head_dim=0), dict(sequences=0),
+    dict(dtype=2), dict(causal=2), dict(tokens_q=-1), dict(tokens_k=-1), dict(scale=0.0),
+    dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(q_token=-1),
+    dict(k_head=-1), dict(q=None), dict(k=None), dict(cu_q=None), dict(cu_k=None)])
+def test_smax_refused(lib, handle, over):
+    assert _smax_call(lib, handle, _qk(**over)) == INVALID
+
+
+def test_smax_arguments_refused(lib, handle):
+    assert _smax_call(lib, None, _qk()) == INVALID
+    assert _smax_call(lib, handle, _qk(), q=None, k=None) == INVALID
+    assert _smax_call(lib, handle, _qk(), accumulate=2) == INVALID
+    assert _smax_call(lib, handle, _qk(), ws=None) == WORKSPACE
+    assert _smax_call(lib, handle, _qk(), ws=6 * BUF + 64) == WORKSPACE
+    assert _smax_call(lib, handle, _qk(), nbytes=16) == WORKSPACE
+    for over in (dict(q=BUF + 1), dict(k=BUF + 1), dict(cu_q=BUF + 2), dict(cu_k=BUF + 2)):
+        assert _smax_call(lib, handle, _qk(**over)) == UNALIGNED
+    assert _smax_call(lib, handle, _qk(), q=BUF + 2) == UNALIGNED
+
+
+def test_smax_workspace_holds_every_partial(lib, handle):
+    sz = ctypes.c_size_t()
+    for tq, seqs, heads in ((1, 1, 1), (10, 2, 4), (5000, 33, 64), (0, 1, 2)):
+        qk = _qk(tokens_q=tq, sequences=seqs, heads_q=heads, heads_k=1)
+        assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(qk), ctypes.byref(sz)) == 0
+        assert sz.value % 256 == 0 and sz.value >= 4 * heads * (tq // 256)
