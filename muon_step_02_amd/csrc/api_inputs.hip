@@ -377,7 +377,8 @@ muon_status muon_expert_grad_weight(muon_handle h, const muon_experts* grads, co
 
 namespace {
 
-muon_status check_qk(const muon_qk* s, SmaxCall* c, muon_handle h) {
+// parts: the most partial maxima either kernel's plan has for these sizes.
+muon_status check_qk(const muon_qk* s, SmaxCall* c, int64_t* parts, muon_handle h) {
     if (!s) return MUON_ERR_INVALID_ARG;
     if (s->heads_q < 1 || s->heads_k < 1 || s->heads_q % s->heads_k || s->heads_q > 65536 ||
         s->head_dim < 1 || s->head_dim > 65536 || s->sequences < 1 || s->sequences > (1 << 20) ||
@@ -407,14 +408,13 @@ muon_status check_qk(const muon_qk* s, SmaxCall* c, muon_handle h) {
     c->bf16 = s->dtype == MUON_BF16;
     c->causal = s->causal;
     c->scale = s->scale;
-    smax_plan(*c, 8 * h->cus_per_xcd);
-    if (!grid_fits(c->qtiles, c->splits, c->heads_q)) return MUON_ERR_INVALID_ARG;
-    return MUON_OK;
+    const bool fast = smax_chunked(*c);
+    *parts = smax_plan(*c, 8 * h->cus_per_xcd, !fast);
+    *parts = std::max(*parts, smax_plan(*c, 8 * h->cus_per_xcd, fast));
+    return *parts > INT32_MAX ? MUON_ERR_INVALID_ARG : MUON_OK;
 }
 
-size_t smax_workspace_bytes(const SmaxCall& c) {
-    return align_up((size_t)c.qtiles * c.splits * c.heads_q * sizeof(float) + 256, 256);
-}
+size_t smax_workspace_bytes(int64_t parts) { return align_up((size_t)parts * sizeof(float) + 256, 256); }
 
 }  // namespace
 
@@ -423,9 +423,10 @@ extern "C" {
 muon_status muon_qk_smax_workspace_size(muon_handle h, const muon_qk* qk, size_t* bytes) {
     if (!h || !bytes) return MUON_ERR_INVALID_ARG;
     SmaxCall c{};
-    const muon_status st = check_qk(qk, &c, h);
+    int64_t parts = 0;
+    const muon_status st = check_qk(qk, &c, &parts, h);
     if (st != MUON_OK) return st;
-    *bytes = smax_workspace_bytes(c);
+    *bytes = smax_workspace_bytes(parts);
     return MUON_OK;
 }
 
@@ -433,7 +434,8 @@ muon_status muon_qk_smax(muon_handle h, const muon_qk* qk, float* smax_q, float*
                          void* workspace, size_t workspace_bytes, void* stream) {
     if (!h) return MUON_ERR_INVALID_ARG;
     SmaxCall c{};
-    const muon_status st = check_qk(qk, &c, h);
+    int64_t parts = 0;
+    const muon_status st = check_qk(qk, &c, &parts, h);
     if (st != MUON_OK) return st;
     if (!smax_q && !smax_k) return MUON_ERR_INVALID_ARG;
     if (accumulate != 0 && accumulate != 1) return MUON_ERR_INVALID_ARG;
@@ -442,7 +444,7 @@ muon_status muon_qk_smax(muon_handle h, const muon_qk* qk, float* smax_q, float*
     if (misaligned(c.q, es) || misaligned(c.k, es) || misaligned(c.cu_q, 4) || misaligned(c.cu_k, 4) ||
         misaligned(smax_q, 4) || misaligned(smax_k, 4))
         return MUON_ERR_UNALIGNED;
-    if (!workspace || misaligned(workspace, 256) || workspace_bytes < smax_workspace_bytes(c))
+    if (!workspace || misaligned(workspace, 256) || workspace_bytes < smax_workspace_bytes(parts))
         return MUON_ERR_WORKSPACE;
     DeviceGuard g(h->device);
     return hip_status(launch_smax(c, reinterpret_cast<float*>(workspace), smax_q, smax_k, accumulate,

@@ -14,8 +14,11 @@
 // the same bits.  A NaN logit makes the head's maximum NaN; a pair that the
 // mask excludes never counts, whatever its values.  A head without any pair
 // gets -inf, which clips nothing.
+#include <algorithm>
+
 #include "inputs.h"
 #include "tile_any.h"
+#include "tile_bf16.h"
 
 namespace muon {
 
@@ -23,7 +26,7 @@ namespace {
 
 // the larger one, NaN if either is
 __device__ __forceinline__ float max_nan(float a, float b) {
-    return (a > b || a != a) ? a : b;
+    return __builtin_elementwise_maximum(a, b);  // v_maximum3_f32
 }
 
 struct Query {
@@ -84,7 +87,7 @@ __device__ __forceinline__ float block_max(float m, float* red) {
 }
 
 // Any type, alignment and head size: 64 x 64 tiles in fp32.  Block -> (query
-// tile, key split, head); split s takes the key tiles s, s + splits, ...
+// tile, key chunk, head).
 __global__ __launch_bounds__(256) void smax_any_kernel(SmaxCall c, float* partials) {
     __shared__ any::Lds lds;
     __shared__ float red[4];
@@ -104,7 +107,7 @@ __global__ __launch_bounds__(256) void smax_any_kernel(SmaxCall c, float* partia
         const int end = c.causal ? min(Lk, i0 + nq + shift) : Lk;
         const any::Operand q{at(c.q, c.bf16, (int64_t)(g.q0 + i0) * c.q_token + (int64_t)h * c.q_head),
                              c.q_token, nq};
-        for (int j0 = split * kSmaxTile; j0 < end; j0 += c.splits * kSmaxTile) {
+        for (int j0 = split * c.chunk; j0 < min(end, (split + 1) * c.chunk); j0 += kSmaxTile) {
             const int nk = min(kSmaxTile, Lk - j0);
             const any::Operand k{at(c.k, c.bf16, (int64_t)(g.k0 + j0) * c.k_token + (int64_t)hk * c.k_head),
                                  c.k_token, nk};
@@ -121,6 +124,158 @@ __global__ __launch_bounds__(256) void smax_any_kernel(SmaxCall c, float* partia
     m = block_max(m, red);
     // the scale is positive: it may follow the maximum
     if (threadIdx.x == 0) gst(partials + (int64_t)h * c.qtiles * c.splits + t * c.splits + split, m * c.scale);
+}
+
+// bf16, head sizes up to 256: four waves of 32 RW queries each (RB row blocks
+// of 32), the queries in registers for the whole run over the keys.  Keys
+// come in tiles of 64 through three LDS stages, copied two tiles ahead: rows
+// of 64-wide sub-slabs (tile_bf16.h), one barrier a tile.  Each key fragment
+// read from LDS feeds RB MFMAs.  Query rows behind the last one repeat it and
+// keys behind the last one repeat it too: a repeated logit changes no
+// maximum, so only the tiles on the causal diagonal need a mask.
+//
+// Block -> (head, query tile, key chunk): a chunk is kSmaxChunk keys, so that
+// no workgroup's run is long.  Late query tiles, which see the most keys, come
+// first; where the heads divide by 8, each XCD takes a run of heads, whose
+// keys its L2 then holds.
+constexpr int kSmaxKeys = 64;
+
+template <int DK, int RB>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(DK <= 192 ? 2 : 1)))
+void smax_bf16_kernel(SmaxCall c, float* partials) {
+    constexpr int SUB = (DK + 63) / 64;          // 64-wide sub-slabs of a key row
+    constexpr int KS = DK / 16;                  // MFMA k-steps
+    constexpr int STAGE = SUB * kSmaxKeys * 64;  // bf16 elements
+    constexpr int BM = 128 * RB;
+    __shared__ __attribute__((aligned(1024))) uint16_t s0[STAGE], s1[STAGE], s2[STAGE];
+    __shared__ float red[4];
+    const int per_head = c.qtiles * c.splits;
+    int L = blockIdx.x;
+    if (c.heads_q % 8 == 0) L = (blockIdx.x & 7) * (c.heads_q / 8 * per_head) + (blockIdx.x >> 3);
+    const int h = L / per_head, rest = L - h * per_head;
+    const int t = rest / c.splits, split = rest - t * c.splits;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float top = -INFINITY;
+    Query g;
+    // tiles are counted from the last one: the last query tile of the last
+    // sequence comes first, tiles that no sequence fills come last
+    if (find_query<BM>(c, t, g)) {
+        const int Lq = g.q1 - g.q0, Lk = g.k1 - g.k0;
+        const int i0 = ((Lq + BM - 1) / BM - 1 - g.tile) * BM;  // late tiles first
+        const int shift = Lk - Lq;
+        const int nq = min(BM, Lq - i0);
+        const int end_all = c.causal ? min(Lk, i0 + nq + shift) : Lk;
+        const int begin = split * c.chunk, end = min(end_all, begin + c.chunk);
+        if (begin < end) {
+            const int D = c.head_dim;
+            const uint16_t* qb = reinterpret_cast<const uint16_t*>(c.q) + (int64_t)h * c.q_head;
+            const int hk = h / (c.heads_q / c.heads_k);
+            const uint16_t* kb = reinterpret_cast<const uint16_t*>(c.k) + (int64_t)hk * c.k_head;
+            // the wave's queries: row block r, k-step s
+            bf::bf16x8 a[RB][KS];
+            int row[RB];
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+                row[r] = min(i0 + wave * 32 * RB + 32 * r + (lane & 31), Lq - 1);
+                const uint16_t* src = qb + (int64_t)(g.q0 + row[r]) * c.q_token + 8 * (lane >> 5);
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (16 * s + 8 * (lane >> 5) < D) v = gld(reinterpret_cast<const uint4*>(src + 16 * s));
+                    a[r][s] = __builtin_bit_cast(bf::bf16x8, v);
+                }
+            }
+            // key tile at j0 into a stage: wave w copies 16 keys of every sub-slab
+            auto copy = [&](int j0, uint16_t* stage) {
+                const uint16_t* base = kb + (int64_t)(g.k0 + j0) * c.k_token;
+                const int last = Lk - 1 - j0;  // >= 0
+                const __amdgpu_buffer_rsrc_t r = bf::resource(base, 0x7fffffff);
+#pragma unroll
+                for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int grp = wave * 2 + q;
+                        const int key = grp * 8 + (lane >> 3);
+                        const int ch = (lane & 7) ^ bf::swz(key);
+                        const uint32_t off = u * 64 + ch * 8 < D
+                            ? (uint32_t)(min(key, last) * (int)c.k_token + u * 64 + ch * 8) * 2u : 0x80000000u;
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                            r, (bf::lds_void*)(stage + (u * kSmaxKeys + grp * 8) * 64), 16, off, 0, 0, 0);
+                    }
+            };
+            constexpr int CPS = 2 * SUB;  // copies of a wave and stage
+            // first and last key that every / any of the wave's queries sees
+            const int wi0 = i0 + wave * 32 * RB;
+            const int every = c.causal ? min(wi0, Lq - 1) + shift : Lk - 1;
+            const int any = c.causal ? min(wi0 + 32 * RB - 1, Lq - 1) + shift : Lk - 1;
+            auto tile = [&](int j0, const uint16_t* stage) {
+                if (j0 > any) return;
+                bf::f32x16 acc[RB][2];
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) acc[r][j][e] = 0.f;
+                bf::bf16x8 b[2][2];
+                auto read = [&](int s, bf::bf16x8 (&f)[2]) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        f[j] = bf::frag_rows(stage + (s / 4) * kSmaxKeys * 64, 32 * j + (lane & 31),
+                                             2 * (s % 4) + (lane >> 5));
+                };
+                read(0, b[0]);
+#pragma unroll
+                for (int s = 0; s < KS; ++s) {
+                    if (s + 1 < KS) read(s + 1, b[(s + 1) & 1]);
+#pragma unroll
+                    for (int r = 0; r < RB; ++r)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            acc[r][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[s & 1][j], a[r][s], acc[r][j], 0, 0, 0);
+                }
+                // operands exchanged: register e of lane l is key 8 (e / 4) +
+                // 4 (l / 32) + e % 4 of the block, query l % 32
+                if (j0 + kSmaxKeys - 1 > every) {
+#pragma unroll
+                    for (int r = 0; r < RB; ++r)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int key = j0 + 32 * j + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3);
+                                const int lim = c.causal ? row[r] + shift : Lk - 1;
+                                if (key > lim) acc[r][j][e] = -INFINITY;
+                            }
+                }
+                float m[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int r = 0; r < RB; ++r)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        m[e & 3] = max_nan(max_nan(m[e & 3], acc[r][0][e]), acc[r][1][e]);
+                top = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+            };
+            const int n = (end - begin + kSmaxKeys - 1) / kSmaxKeys;
+            // a copy behind the last key repeats it: every stage may be filled
+            auto start = [&](int i) { return min(begin + i * kSmaxKeys, Lk - 1); };
+            copy(start(0), s0);
+            copy(start(1), s1);
+            for (int i = 0; i < n; i += 3) {
+#pragma unroll
+                for (int u = 0; u < 3; ++u) {
+                    if (i + u >= n) break;
+                    bf::wait_vmcnt<CPS>();  // this tile's copies, not the next one's
+                    bf::lds_barrier();
+                    copy(start(i + u + 2), u == 0 ? s2 : u == 1 ? s0 : s1);
+                    tile(begin + (i + u) * kSmaxKeys, u == 0 ? s0 : u == 1 ? s1 : s2);
+                }
+            }
+            bf::wait_vmcnt<0>();
+        }
+    }
+    top = block_max(top, red);
+    if (threadIdx.x == 0) gst(partials + (int64_t)h * per_head + rest, top * c.scale);
 }
 
 // Partials of a head to its maximum; block: one key head and its query heads.
@@ -143,22 +298,62 @@ __global__ __launch_bounds__(256) void smax_finalize_kernel(const float* partial
 
 }  // namespace
 
-void smax_plan(SmaxCall& c, int cus) {
+// bf16 rows that start on 16 bytes and hold whole 16-byte chunks, of a size
+// that the registers hold
+bool smax_chunked(const SmaxCall& c) {
+    auto ok = [](const void* p, int64_t token, int64_t head) {
+        return reinterpret_cast<uintptr_t>(p) % 16 == 0 && token % 8 == 0 && head % 8 == 0;
+    };
+    return c.bf16 && c.head_dim % 8 == 0 && c.head_dim <= 256 && ok(c.q, c.q_token, c.q_head) &&
+           ok(c.k, c.k_token, c.k_head) && c.k_token <= (1 << 22);
+}
+
+namespace {
+
+template <int DK>
+void smax_launch(const SmaxCall& c, unsigned grid, float* partials, hipStream_t st) {
+    if (c.tile == 256)
+        smax_bf16_kernel<DK, 2><<<grid, 256, 0, st>>>(c, partials);
+    else
+        smax_bf16_kernel<DK, 1><<<grid, 256, 0, st>>>(c, partials);
+}
+
+}  // namespace
+
+int64_t smax_plan(SmaxCall& c, int cus, bool chunked) {
     const int64_t seq = c.sequences < c.tq ? c.sequences : c.tq;
-    c.qtiles = (int)(c.tq / kSmaxTile + seq);
+    // short sequences on tiles of 128 queries
+    c.tile = !chunked ? kSmaxTile : c.tq < (int64_t)kSmaxLong * seq ? 128 : 256;
+    c.qtiles = (int)(c.tq / c.tile + seq);
     // few query tiles: the keys are split too, up to four workgroups a compute unit
     const int64_t have = (int64_t)c.qtiles * c.heads_q, want = 4 * (int64_t)cus;
     const int64_t ktiles = (c.tk + kSmaxTile - 1) / kSmaxTile;
     int64_t s = have > 0 ? want / have : 1;
-    if (s > ktiles) s = ktiles;
-    c.splits = s < 1 ? 1 : (int)s;
+    if (chunked) s = std::max(s, (c.tk + kSmaxChunk - 1) / kSmaxChunk);
+    s = std::max<int64_t>(1, std::min(s, ktiles));
+    // chunks of whole key tiles, and as many splits as they make
+    c.chunk = (int)std::max<int64_t>(1, (ktiles + s - 1) / s) * kSmaxTile;
+    c.splits = (int)std::max<int64_t>(1, (c.tk + c.chunk - 1) / c.chunk);
+    return (int64_t)c.qtiles * c.splits * c.heads_q;
 }
 
 hipError_t launch_smax(const SmaxCall& c, float* partials, float* smax_q, float* smax_k, int accumulate,
                        hipStream_t st) {
     const int per_head = c.qtiles * c.splits;
     if (per_head > 0) {
-        smax_any_kernel<<<(unsigned)(per_head * (int64_t)c.heads_q), 256, 0, st>>>(c, partials);
+        const unsigned grid = (unsigned)(per_head * (int64_t)c.heads_q);
+        if (c.tile == kSmaxTile)
+            smax_any_kernel<<<grid, 256, 0, st>>>(c, partials);
+        else if (c.head_dim <= 64)
+            smax_launch<64>(c, grid, partials, st);
+        else if (c.head_dim <= 96)
+            smax_launch<96>(c, grid, partials, st);
+        else if (c.head_dim <= 128)
+            smax_launch<128>(c, grid, partials, st);
+        else if (c.head_dim <= 192)
+            smax_launch<192>(c, grid, partials, st);
+        else
+            smax_launch<256>(c, grid, partials, st);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -171,6 +171,16 @@ __device__ __forceinline__ void wait_vmcnt() {
     __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
 }
 
+// Workgroup barrier without a memory fence: the wave's own LDS reads are
+// waited for, copies in flight stay in flight (__syncthreads() would wait for
+// them).
+__device__ __forceinline__ void lds_barrier() {
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0) only
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+}
+
 // The LDS reads of the next k-step go out two at a time between the first
 // MFMAs of this one.
 template <int NR, int NM, int T = 0>
