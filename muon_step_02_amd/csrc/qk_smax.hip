@@ -196,7 +196,7 @@ void smax_bf16_kernel(SmaxCall c, float* partials) {
                     for (int q = 0; q < 2; ++q) {
                         const int grp = wave * 2 + q;
                         const int key = grp * 8 + (lane >> 3);
-                        const int ch = (lane & 7) ^ bf::swz(key);
+                        const int ch = (lane & 7) ^ bf::swz<64>(key);
                         const uint32_t off = u * 64 + ch * 8 < D
                             ? (uint32_t)(min(key, last) * (int)c.k_token + u * 64 + ch * 8) * 2u : 0x80000000u;
                         __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -221,7 +221,7 @@ void smax_bf16_kernel(SmaxCall c, float* partials) {
                 auto read = [&](int s, bf::bf16x8 (&f)[2]) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        f[j] = bf::frag_rows(stage + (s / 4) * kSmaxKeys * 64, 32 * j + (lane & 31),
+                        f[j] = bf::frag_rows<64>(stage + (s / 4) * kSmaxKeys * 64, 32 * j + (lane & 31),
                                              2 * (s % 4) + (lane >> 5));
                 };
                 read(0, b[0]);

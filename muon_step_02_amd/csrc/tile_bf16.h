@@ -4,7 +4,7 @@
 //
 // A workgroup of WM x WN waves computes BM x BN, each wave a block of 32 x 32
 // MFMA tiles (v_mfma_f32_32x32x16_bf16, fp32 accumulation).  K advances in
-// slabs of 64, copied global -> LDS with buffer_load_dwordx4 ... lds (16 bytes
+// slabs of BK (32 or 64), copied global -> LDS with buffer_load_dwordx4 ... lds (16 bytes
 // per lane, no registers in between).  The copies go through buffer resources
 // that end where the operand does: a row or k behind the end reads as zero,
 // so ragged ends need no branch and no memory traffic, and a value that lies
@@ -14,6 +14,8 @@
 // tile's rows) or k-major (rows are k).  k-major slabs are copied as they are
 // and gathered with the transposing LDS read (ds_read_b64_tr_b16).
 #pragma once
+
+#include <utility>
 
 #include "muon_internal.h"
 
@@ -25,20 +27,22 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
-constexpr int kBK = 64;      // k per slab
-constexpr int kSlab = 16384;  // bf16 elements of an LDS array (256 rows)
-
-// PKM, QKM: the operand is stored k-major.
-template <int BM_, int BN_, int WM_, int WN_, bool PKM_, bool QKM_>
+// PKM, QKM: the operand is stored k-major.  BK: k per slab; NS: LDS stages.
+// RB: rows of an epilogue band, 32 or 16 (RB x BN floats fit one stage array).
+template <int BM_, int BN_, int WM_, int WN_, bool PKM_, bool QKM_, int BK_ = 64, int NS_ = 2, int RB_ = 32>
 struct Cfg {
+    static constexpr int BK = BK_, NS = NS_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
     static constexpr bool PKM = PKM_, QKM = QKM_;
     static constexpr int NW = WM * WN, NT = 64 * NW;
     static constexpr int TM = BM / WM, TN = BN / WN;
     static constexpr int FM = TM / 32, FN = TN / 32;
-    static constexpr int RB = 32;  // rows of an epilogue band
-    static_assert(FM >= 1 && FN >= 1 && BM % 64 == 0 && BN % 64 == 0, "32 x 32 blocks per wave");
-    static_assert((BM / 8) % NW == 0 && (BN / 8) % NW == 0, "slab copies split evenly over the waves");
+    static constexpr int RB = RB_;
+    static constexpr int CH = BK / 8;                          // 16-byte chunks of a K-contiguous row
+    static constexpr int LPS = (BM + BN) * BK / 512 / NW;      // copies of a wave and stage
+    static_assert(FM >= 1 && FN >= 1 && BM % 32 == 0 && BN % 64 == 0, "32 x 32 blocks per wave");
+    static_assert(BM * BK / 512 % NW == 0 && BN * BK / 512 % NW == 0, "slab copies split evenly over the waves");
+    static_assert((BK == 32 || BK == 64) && NS >= 2 && NS <= 5 && (RB == 16 || RB == 32), "");
     static_assert(RB * BN % (8 * NT) == 0, "epilogue chunks split evenly over the threads");
 };
 
@@ -56,50 +60,55 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t resource(const uint16_t* base,
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t*>(base), 0, n, 0x00020000);
 }
 
-// LDS slab of a K-contiguous operand: 64 bf16 (8 chunks of 16 bytes) per row,
-// chunk c at position c ^ swz(row): the 16 lanes of one LDS cycle read one
+// LDS slab of a K-contiguous operand: BK bf16 (8 or 4 chunks of 16 bytes) per
+// row, chunk c at position c ^ swz(row): the 16 lanes of one LDS cycle read one
 // chunk of 16 consecutive rows, on 16 different positions of the 64 banks.
-__device__ __forceinline__ int swz(int row) { return (row >> 1) & 7; }
+template <int BK = 64>
+__device__ __forceinline__ int swz(int row) { return BK == 64 ? (row >> 1) & 7 : (row >> 2) & 3; }
 // k-major slab of W columns: chunk c of row k at c ^ swzk(k): the 4 rows x 64
-// bytes of a transposing read lie on disjoint quarters of the banks.
-__device__ __forceinline__ int swzk(int k) { return (k & 3) << 2; }
+// bytes of a transposing read lie on disjoint quarters of the banks (a row of
+// 64 columns is half of them).
+template <int W>
+__device__ __forceinline__ int swzk(int k) { return W == 64 ? (k & 2) << 1 : (k & 3) << 2; }
 
-// Copies of k [k0, k0 + 64) of R rows into an LDS slab; NW waves share them.
-// Lane l of a copy fills chunk position l % 8 of row l / 8.
-template <int R, int NW>
+// Copies of k [k0, k0 + BK) of R rows into an LDS slab; NW waves share them.
+// Lane l of a copy fills chunk position l % CH of row l / CH.
+template <int R, int NW, int BK>
 __device__ __forceinline__ void copy_rows(const Operand& o, int64_t k0, int64_t K, uint16_t* slab, int wave,
                                           int lane) {
+    constexpr int CH = BK / 8, RPC = 64 / CH;  // chunks of a row, rows of a copy
     const __amdgpu_buffer_rsrc_t r = resource(o.base + k0, o.bytes - 2 * k0);
-    const int left = K - k0 < kBK ? (int)(K - k0) : kBK;  // a multiple of 8
+    const int left = K - k0 < BK ? (int)(K - k0) : BK;  // a multiple of 8
 #pragma unroll
-    for (int q = 0; q < R / 8 / NW; ++q) {
-        const int grp = wave * (R / 8 / NW) + q;
-        const int row = grp * 8 + (lane >> 3);
-        const int c = (lane & 7) ^ swz(row);
+    for (int q = 0; q < R / RPC / NW; ++q) {
+        const int grp = wave * (R / RPC / NW) + q;
+        const int row = grp * RPC + lane / CH;
+        const int c = (lane % CH) ^ swz<BK>(row);
         // a chunk behind K would be the next row's: pushed out of range
         const uint32_t off = c * 8 < left ? (uint32_t)(row * (int)o.ld + c * 8) * 2u : 0x80000000u;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(slab + grp * 8 * kBK), 16, off, 0, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(slab + grp * RPC * BK), 16, off, 0, 0, 0);
     }
 }
 
-// ... of a k-major operand: 64 rows k of W columns.
-template <int W, int NW>
+// ... of a k-major operand: BK rows k of W columns.
+template <int W, int NW, int BK>
 __device__ __forceinline__ void copy_kmajor(const Operand& o, int64_t k0, uint16_t* slab, int wave, int lane) {
     constexpr int CQ = W / 8, RPK = 64 / CQ;  // chunks of a row, rows of a copy
-    static_assert(CQ <= 64 && (kBK / RPK) % NW == 0, "k-major copies split evenly over the waves");
+    static_assert(CQ <= 64 && (BK / RPK) % NW == 0, "k-major copies split evenly over the waves");
     const __amdgpu_buffer_rsrc_t r = resource(o.base + k0 * o.ld, o.bytes - 2 * k0 * o.ld);
 #pragma unroll
-    for (int q = 0; q < kBK / RPK / NW; ++q) {
-        const int grp = wave * (kBK / RPK / NW) + q;
+    for (int q = 0; q < BK / RPK / NW; ++q) {
+        const int grp = wave * (BK / RPK / NW) + q;
         const int k = grp * RPK + lane / CQ;
-        const uint32_t off = (uint32_t)(k * (int)o.ld + (((lane % CQ) ^ swzk(k)) * 8)) * 2u;
+        const uint32_t off = (uint32_t)(k * (int)o.ld + (((lane % CQ) ^ swzk<W>(k)) * 8)) * 2u;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(slab + grp * RPK * W), 16, off, 0, 0, 0);
     }
 }
 
 // MFMA operand fragment: lane l holds row l % 32, k = 8 (l / 32) + 0..7.
+template <int BK = 64>
 __device__ __forceinline__ bf16x8 frag_rows(const uint16_t* slab, int row, int chunk) {
-    return *reinterpret_cast<const bf16x8*>(slab + row * kBK + ((chunk ^ swz(row)) << 3));
+    return *reinterpret_cast<const bf16x8*>(slab + row * BK + ((chunk ^ swz<BK>(row)) << 3));
 }
 // ... from a k-major slab of W columns, as two transposing 8-byte reads: in
 // each group of 16 lanes, lane a + 4 b addresses row b, columns 4a ... 4a + 3
@@ -112,16 +121,18 @@ __device__ __forceinline__ bf16x8 frag_kmajor(const uint16_t* slab, int k0, int 
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         const int k = k0 + 8 * (g >> 1) + 4 * t + (s16 >> 2);
-        const uint16_t* p = slab + k * W + (((n >> 3) ^ swzk(k)) << 3) + (n & 7);
+        const uint16_t* p = slab + k * W + (((n >> 3) ^ swzk<W>(k)) << 3) + (n & 7);
         h[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) i16x4*)(p));
     }
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(h[0], h[1], 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
-// Two stages of one array per operand, each its own __shared__ variable: the
-// compiler then knows that a copy into one leaves the others alone.
+// LDS stages, one array per operand and stage, each its own __shared__
+// variable: the compiler then knows that a copy into one leaves the others
+// alone.
+template <int NS>
 struct Stages {
-    uint16_t *p0, *q0, *p1, *q1;
+    uint16_t *p[NS], *q[NS];
 };
 
 template <class C>
@@ -136,11 +147,11 @@ __device__ __forceinline__ void read_frags(const uint16_t* sp, const uint16_t* s
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
         f.a[i] = C::PKM ? frag_kmajor<C::BM>(sp, 16 * kk, wm * C::TM + i * 32, lane)
-                        : frag_rows(sp, wm * C::TM + i * 32 + row, chunk);
+                        : frag_rows<C::BK>(sp, wm * C::TM + i * 32 + row, chunk);
 #pragma unroll
     for (int j = 0; j < C::FN; ++j)
         f.b[j] = C::QKM ? frag_kmajor<C::BN>(sq, 16 * kk, wn * C::TN + j * 32, lane)
-                        : frag_rows(sq, wn * C::TN + j * 32 + row, chunk);
+                        : frag_rows<C::BK>(sq, wn * C::TN + j * 32 + row, chunk);
 }
 
 template <class C>
@@ -156,13 +167,13 @@ template <class C>
 __device__ __forceinline__ void copy_stage(const Operand& p, const Operand& q, int64_t k0, int64_t K,
                                            uint16_t* sp, uint16_t* sq, int wave, int lane) {
     if constexpr (C::PKM)
-        copy_kmajor<C::BM, C::NW>(p, k0, sp, wave, lane);
+        copy_kmajor<C::BM, C::NW, C::BK>(p, k0, sp, wave, lane);
     else
-        copy_rows<C::BM, C::NW>(p, k0, K, sp, wave, lane);
+        copy_rows<C::BM, C::NW, C::BK>(p, k0, K, sp, wave, lane);
     if constexpr (C::QKM)
-        copy_kmajor<C::BN, C::NW>(q, k0, sq, wave, lane);
+        copy_kmajor<C::BN, C::NW, C::BK>(q, k0, sq, wave, lane);
     else
-        copy_rows<C::BN, C::NW>(q, k0, K, sq, wave, lane);
+        copy_rows<C::BN, C::NW, C::BK>(q, k0, K, sq, wave, lane);
 }
 
 template <int N>
@@ -195,63 +206,77 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-// acc = the tile over k [0, K).  Both stages are filled up front; while the
-// MFMAs of a k-step (16 deep) run, the fragments of the next are read into
-// the other registers.  The last k-step's MFMAs are issued after the barrier
-// that frees the slab's stage, so the matrix cores have work while the waves
-// meet; the copy of slab kt + 2 goes into that stage.
+// f(integral_constant 0), ..., f(integral_constant N - 1): indices that are
+// constants before any loop is unrolled, so that every LDS access names its
+// array (an access that could be to any array waits for every copy in flight).
+template <class F, int... I>
+__device__ __forceinline__ void unrolled_(F&& f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F&& f) {
+    unrolled_(f, std::make_integer_sequence<int, N>{});
+}
+
 template <class C>
-__device__ __forceinline__ void product(f32x16 (&acc)[C::FM][C::FN], const Operand& p, const Operand& q,
-                                        int64_t K, const Stages& st) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int wm = wave / C::WN, wn = wave % C::WN;
+__device__ __forceinline__ void zero(f32x16 (&acc)[C::FM][C::FN]) {
 #pragma unroll
     for (int i = 0; i < C::FM; ++i)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
 #pragma unroll
             for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    const int KT = (int)((K + kBK - 1) / kBK);
+}
+
+// acc += the tile over k [0, K).  All stages are filled up front; while the
+// MFMAs of a k-step (16 deep) run, the fragments of the next are read into
+// the other registers.  The last k-step's MFMAs are issued after the barrier
+// that frees the slab's stage, so the matrix cores have work while the waves
+// meet; the copy of slab kt + NS goes into that stage.  Copies in flight stay
+// in flight at the barriers.
+template <class C>
+__device__ __forceinline__ void product(f32x16 (&acc)[C::FM][C::FN], const Operand& p, const Operand& q,
+                                        int64_t K, const Stages<C::NS>& st) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const int KT = (int)((K + C::BK - 1) / C::BK);
     if (KT == 0) return;
-    constexpr int KS = kBK / 16;
+    constexpr int KS = C::BK / 16, NS = C::NS;
     constexpr int NR = (C::PKM ? 2 : 1) * C::FM + (C::QKM ? 2 : 1) * C::FN;
-    copy_stage<C>(p, q, 0, K, st.p0, st.q0, wave, lane);
-    // behind K every copy reads zeros: the second stage is filled either way
-    copy_stage<C>(p, q, kBK, K, st.p1, st.q1, wave, lane);
-    constexpr int LPS = (C::BM / 8 + C::BN / 8) / C::NW;
-    wait_vmcnt<LPS>();
-    __syncthreads();
+    // behind K every copy reads zeros, without memory traffic: copies and waits
+    // need no condition (the compiler would wait for the path of a condition
+    // that leaves the most copies in flight)
+    unrolled<NS>([&](auto u) { copy_stage<C>(p, q, u * C::BK, K, st.p[u], st.q[u], wave, lane); });
+    wait_vmcnt<(NS - 1) * C::LPS>();
+    lds_barrier();
     Frags<C> f[2];
-    read_frags<C>(st.p0, st.q0, 0, wm, wn, lane, f[0]);
-    for (int kt0 = 0; kt0 < KT; kt0 += 2) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
+    read_frags<C>(st.p[0], st.q[0], 0, wm, wn, lane, f[0]);
+    for (int kt0 = 0; kt0 < KT; kt0 += NS) {
+        unrolled<NS>([&](auto u) {
+            constexpr int next = (u + 1) % NS;
             const int kt = kt0 + u;
-            if (kt < KT) {
-                uint16_t* const sp = u ? st.p1 : st.p0;
-                uint16_t* const sq = u ? st.q1 : st.q0;
-                const uint16_t* const np = u ? st.p0 : st.p1;
-                const uint16_t* const nq = u ? st.q0 : st.q1;
+            if (kt >= KT) return;
 #pragma unroll
-                for (int kk = 0; kk < KS; ++kk) {
-                    if (kk + 1 < KS) {
-                        read_frags<C>(sp, sq, kk + 1, wm, wn, lane, f[(kk + 1) & 1]);
-                    } else {
-                        wait_vmcnt<0>();
-                        __syncthreads();
-                        if (kt + 2 < KT) copy_stage<C>(p, q, (int64_t)(kt + 2) * kBK, K, sp, sq, wave, lane);
-                        read_frags<C>(np, nq, 0, wm, wn, lane, f[0]);
-                    }
-                    mfma_frags<C>(acc, f[kk & 1]);
-                    interleave<NR, C::FM * C::FN>();
+            for (int kk = 0; kk < KS; ++kk) {
+                if (kk < KS - 1) {
+                    read_frags<C>(st.p[u], st.q[u], kk + 1, wm, wn, lane, f[(kk + 1) & 1]);
+                } else {
+                    // slab kt + 1 has landed once only the copies of the
+                    // slabs after it are outstanding
+                    wait_vmcnt<(NS - 2) * C::LPS>();
+                    lds_barrier();
+                    copy_stage<C>(p, q, (int64_t)(kt + NS) * C::BK, K, st.p[u], st.q[u], wave, lane);
+                    read_frags<C>(st.p[next], st.q[next], 0, wm, wn, lane, f[0]);
                 }
+                mfma_frags<C>(acc, f[kk & 1]);
+                interleave<NR, C::FM * C::FN>();
             }
-        }
+        });
     }
     wait_vmcnt<0>();
 }
 
-// Epilogue band (32 rows in fp32, in LDS): column c of row r at
+// Epilogue band (RB rows in fp32, in LDS): column c of row r at
 // c ^ ((r & 4) << 3) ^ ((r >> 3) << 4), so that the two half-waves of an
 // accumulator store (rows r and r + 4) lie 32 banks apart.
 template <class C>
@@ -259,36 +284,52 @@ __device__ __forceinline__ int band_at(int r, int c) {
     return r * C::BN + (c ^ ((r & 4) << 3) ^ ((r >> 3) << 4));
 }
 
-// Passes the tile row band by row band through LDS (`band`, 32 x BN floats):
-// put(row, column, values) for 8 consecutive columns, column a multiple of 8.
-template <class C, class F>
-__device__ __forceinline__ void for_each_chunk(const f32x16 (&acc)[C::FM][C::FN], float* band, int rows, F&& put) {
+// Chunks of 8 columns that a thread stores per band, and the row and column of
+// its chunk q in band b.
+template <class C>
+constexpr int chunks_per_band() { return C::RB * C::BN / 8 / C::NT; }
+template <class C>
+__device__ __forceinline__ int chunk_row(int b, int q) {
+    return b * C::RB + (q * C::NT + threadIdx.x) / (C::BN / 8);
+}
+template <class C>
+__device__ __forceinline__ int chunk_col(int q) {
+    return (q * C::NT + threadIdx.x) % (C::BN / 8) * 8;
+}
+
+// Passes the tile row band by row band through LDS (`band`, RB x BN floats):
+// put(b, q, row, column, values) for chunk q of band b.  ahead(b) is called
+// before band b is put: loads for band b + 1 belong there.
+template <class C, class A, class F>
+__device__ __forceinline__ void for_each_chunk(const f32x16 (&acc)[C::FM][C::FN], float* band, int rows,
+                                               A&& ahead, F&& put) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / C::WN, wn = wave % C::WN;
 #pragma unroll
     for (int b = 0; b < C::BM / C::RB; ++b) {
         if (b * C::RB >= rows) break;  // uniform
+        ahead(b);
         __syncthreads();
+        constexpr int H = 32 / C::RB;  // bands of a block of 32 rows: 8 registers each of two
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
-            if (wm * C::TM + i * 32 == b * C::RB) {
+            if (wm * C::TM + i * 32 == b / H * 32) {
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                        band[band_at<C>(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), wn * C::TN + j * 32 + (lane & 31))] =
-                            acc[i][j][r];
+                    for (int r = b % H * (16 / H); r < b % H * (16 / H) + 16 / H; ++r)
+                        band[band_at<C>((8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) % C::RB,
+                                        wn * C::TN + j * 32 + (lane & 31))] = acc[i][j][r];
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < C::RB * C::BN / 8 / C::NT; ++q) {
-            const int ch = q * C::NT + threadIdx.x;
-            const int rr = ch / (C::BN / 8), c8 = (ch % (C::BN / 8)) * 8;
+        for (int q = 0; q < chunks_per_band<C>(); ++q) {
+            const int rr = chunk_row<C>(0, q), c8 = chunk_col<C>(q);
             const float4 a0 = *reinterpret_cast<const float4*>(band + band_at<C>(rr, c8));
             const float4 a1 = *reinterpret_cast<const float4*>(band + band_at<C>(rr, c8) + 4);
             const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            put(b * C::RB + rr, c8, v);
+            put(b, q, b * C::RB + rr, c8, v);
         }
     }
     __syncthreads();
