@@ -98,15 +98,13 @@ struct SmaxCall {
     int32_t bf16, causal;
     float scale;
     int32_t tile;            // queries of a tile
-    int32_t qtiles, splits;  // bound of query tiles over all sequences, key chunks
-    int32_t chunk;           // keys of a chunk, a multiple of kSmaxTile
+    int32_t qtiles, splits;  // bound of query tiles over all sequences, key parts of each
 };
-constexpr int kSmaxTile = 64;  // queries (and keys) per tile of the kernel for any type
-constexpr int kSmaxChunk = 2048;  // most keys of a chunk on the bf16 kernels
-constexpr int kSmaxLong = 512;    // mean queries of a sequence from which tiles hold 256
+constexpr int kSmaxTile = 64;   // queries (and keys) per tile of the kernel for any type
+constexpr int kSmaxLong = 512;  // mean queries of a sequence from which tiles hold 256
 // whether the bf16 kernels take the call (the one for any type takes all)
 bool smax_chunked(const SmaxCall& c);
-// fills tile, qtiles, splits and chunk from the sizes, for the bf16 kernels or
+// fills tile, qtiles and splits from the sizes, for the bf16 kernels or
 // for the other one; returns the number of partial maxima
 int64_t smax_plan(SmaxCall& c, int cus, bool chunked);
 hipError_t launch_smax(const SmaxCall& c, float* partials, float* smax_q, float* smax_k,
