@@ -15,69 +15,84 @@
 // the loads take), and no gradient that fp32 can hold overflows or vanishes
 // in its square.  Every sum has a fixed order, so results are bitwise
 // repeatable: block b takes chunks b, b + blocks, ... of the group.
+#include <type_traits>
+
 #include "inputs.h"
 
 namespace muon {
 
 namespace {
 
-// 16 bytes at the alignment of an element: rows of any leading dimension are
-// read with full-width loads (gfx950 allows unaligned global accesses).
-typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
-typedef uint16_t u16x8u __attribute__((ext_vector_type(8), aligned(2)));
-typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
+// 16 or 8 bytes at the alignment of an element: rows of any leading dimension
+// are read with full-width loads (gfx950 allows unaligned global accesses).
+typedef uint32_t u32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2h __attribute__((ext_vector_type(2), aligned(2)));
 
-constexpr int kQ = kGradUnits / 256;  // units per thread and chunk
-
-template <bool BF>
-struct Elems {
-    static constexpr int V = BF ? 8 : 4;  // elements of a unit
-    float v[V];
+// V elements of a row as they are in memory.
+template <bool BF, int V>
+struct Raw {
+    static constexpr int W = BF ? V / 2 : V;  // 32-bit words
+    uint32_t w[W];
+    __device__ __forceinline__ float at(int e) const {
+        if (!BF) return __builtin_bit_cast(float, w[e]);
+        return __builtin_bit_cast(float, (e & 1) ? (w[e / 2] & 0xffff0000u) : (w[e / 2] << 16));
+    }
 };
 
-// The unit at element offset `off`; `left`: elements the row still holds.
-template <bool BF>
-__device__ __forceinline__ Elems<BF> load_unit(const void* base, int64_t off, int64_t left) {
-    Elems<BF> r;
-    constexpr int V = Elems<BF>::V;
-    if (left >= V) {
-        if constexpr (BF) {
-            const u16x8u u = *(const MUON_GLOBAL u16x8u*)(reinterpret_cast<const uint16_t*>(base) + off);
+// The V elements at offset `off`; `left`: elements the row still holds.  FULL:
+// at least V of them, known without looking.
+template <bool BF, int V, bool FULL>
+__device__ __forceinline__ Raw<BF, V> load_raw(const void* base, int64_t off, int64_t left) {
+    Raw<BF, V> r;
+    if (FULL || left >= V) {
+        if constexpr (!BF) {
+            const u32x4u u = *(const MUON_GLOBAL u32x4u*)(reinterpret_cast<const float*>(base) + off);
 #pragma unroll
-            for (int e = 0; e < V; ++e) r.v[e] = bf16_bits_to_f32(u[e]);
+            for (int i = 0; i < 4; ++i) r.w[i] = u[i];
+        } else if constexpr (V == 8) {
+            const u32x4h u = *(const MUON_GLOBAL u32x4h*)(reinterpret_cast<const uint16_t*>(base) + off);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r.w[i] = u[i];
         } else {
-            const f32x4u u = *(const MUON_GLOBAL f32x4u*)(reinterpret_cast<const float*>(base) + off);
-#pragma unroll
-            for (int e = 0; e < V; ++e) r.v[e] = u[e];
+            const u32x2h u = *(const MUON_GLOBAL u32x2h*)(reinterpret_cast<const uint16_t*>(base) + off);
+            r.w[0] = u[0];
+            r.w[1] = u[1];
         }
     } else {
 #pragma unroll
+        for (int i = 0; i < Raw<BF, V>::W; ++i) r.w[i] = 0;
+#pragma unroll
         for (int e = 0; e < V; ++e) {
-            r.v[e] = 0.f;
-            if (e < left)
-                r.v[e] = BF ? bf16_bits_to_f32(gld(reinterpret_cast<const uint16_t*>(base) + off + e))
-                            : gld(reinterpret_cast<const float*>(base) + off + e);
+            if (e < left) {
+                if (BF)
+                    r.w[e / 2] |= (uint32_t)gld(reinterpret_cast<const uint16_t*>(base) + off + e) << 16 * (e & 1);
+                else
+                    r.w[e] = gld(reinterpret_cast<const uint32_t*>(base) + off + e);
+            }
         }
     }
     return r;
 }
 
-template <int V, bool OBF>
+template <int V, bool OBF, bool FULL>
 __device__ __forceinline__ void store_unit(void* base, int64_t off, int64_t left, const float* v) {
-    if (left >= V) {
+    if (FULL || left >= V) {
+        if constexpr (!OBF) {
+            u32x4u o;
 #pragma unroll
-        for (int h = 0; h < V / 4; ++h) {
-            if constexpr (OBF) {
-                u16x4u o;
+            for (int e = 0; e < 4; ++e) o[e] = __builtin_bit_cast(uint32_t, v[e]);
+            *(MUON_GLOBAL u32x4u*)(reinterpret_cast<float*>(base) + off) = o;
+        } else {
+            uint32_t w[V / 2];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = f32_to_bf16_bits(v[4 * h + e]);
-                *(MUON_GLOBAL u16x4u*)(reinterpret_cast<uint16_t*>(base) + off + 4 * h) = o;
-            } else {
-                f32x4u o;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[e] = v[4 * h + e];
-                *(MUON_GLOBAL f32x4u*)(reinterpret_cast<float*>(base) + off + 4 * h) = o;
-            }
+            for (int i = 0; i < V / 2; ++i)
+                w[i] = (uint32_t)f32_to_bf16_bits(v[2 * i]) | (uint32_t)f32_to_bf16_bits(v[2 * i + 1]) << 16;
+            uint16_t* p = reinterpret_cast<uint16_t*>(base) + off;
+            if constexpr (V == 8)
+                *(MUON_GLOBAL u32x4h*)p = u32x4h{w[0], w[1], w[2], w[3]};
+            else
+                *(MUON_GLOBAL u32x2h*)p = u32x2h{w[0], w[1]};
         }
     } else {
 #pragma unroll
@@ -138,66 +153,87 @@ struct Walk {
     }
 };
 
-template <bool BF>
+// Whether every unit of a chunk is whole: then no lane looks at its end.
+__device__ __forceinline__ bool whole(int64_t rows, int64_t cols, int V, int64_t first) {
+    return cols % V == 0 && first + kGradUnits <= rows * (cols / V);
+}
+
+template <bool BF, bool FULL>
 __device__ __forceinline__ void chunk_sumsq(const void* g, int64_t rows, int64_t cols, int64_t ld,
-                                            int64_t first, double (&acc)[4]) {
-    constexpr int V = Elems<BF>::V;
-    Walk w(first + threadIdx.x, (cols + V - 1) / V, rows);
-    Elems<BF> x[kQ];
+                                            int64_t first, int tid, double (&acc)[4]) {
+    constexpr int V = BF ? 8 : 4, Q = kGradUnits / 256;
+    Walk w(first + tid, (cols + V - 1) / V, rows);
+    Raw<BF, V> x[Q];
     // every load first, so that all are in flight together
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-        x[q] = load_unit<BF>(g, w.r * ld + w.c * V, w.inside() ? cols - w.c * V : 0);
+    for (int q = 0; q < Q; ++q) {
+        x[q] = load_raw<BF, V, FULL>(g, w.r * ld + w.c * V, w.inside() ? cols - w.c * V : 0);
         w.next();
     }
 #pragma unroll
-    for (int q = 0; q < kQ; ++q)
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-            const double d = (double)x[q].v[e];
+            const double d = (double)x[q].at(e);
             acc[e & 3] = fma(d, d, acc[e & 3]);
         }
 }
 
-template <bool BF, bool OBF>
+// A chunk in units of 16 bytes of the wider type: bf16 gradients go to an fp32
+// output in half units, so that its stores are whole 16 bytes a lane too.
+template <bool BF, bool OBF, bool FULL>
 __device__ __forceinline__ void chunk_scale(const void* g, void* out, int64_t rows, int64_t cols,
-                                            int64_t ld, int64_t ld_out, int64_t first, float scale) {
-    constexpr int V = Elems<BF>::V;
-    const Walk w0(first + threadIdx.x, (cols + V - 1) / V, rows);
-    Elems<BF> x[kQ];
+                                            int64_t ld, int64_t ld_out, int64_t first, int tid, float scale) {
+    constexpr int H = BF && !OBF ? 2 : 1;  // parts of a unit
+    constexpr int V = (BF ? 8 : 4) / H, Q = kGradUnits / 256 * H;
+    const Walk w0(first * H + tid, (cols + V * H - 1) / (V * H) * H, rows);
+    Raw<BF, V> x[Q];
     Walk w = w0;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {
-        x[q] = load_unit<BF>(g, w.r * ld + w.c * V, w.inside() ? cols - w.c * V : 0);
+    for (int q = 0; q < Q; ++q) {
+        x[q] = load_raw<BF, V, FULL>(g, w.r * ld + w.c * V, w.inside() ? cols - w.c * V : 0);
         w.next();
     }
     w = w0;
 #pragma unroll
-    for (int q = 0; q < kQ; ++q) {
+    for (int q = 0; q < Q; ++q) {
+        float v[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[q].v[e] *= scale;
-        store_unit<V, OBF>(out, w.r * ld_out + w.c * V, w.inside() ? cols - w.c * V : 0, x[q].v);
+        for (int e = 0; e < V; ++e) v[e] = x[q].at(e) * scale;
+        store_unit<V, OBF, FULL>(out, w.r * ld_out + w.c * V, w.inside() ? cols - w.c * V : 0, v);
         w.next();
     }
 }
 
+// Chunks b, b + blocks, ... of a group; tid: the thread's place among the 256
+// that share a chunk.
 template <int CAP>
-__device__ __forceinline__ void group_sumsq(const GradGroup<CAP>& grp, int b, int blocks, double (&acc)[4]) {
+__device__ __forceinline__ void group_sumsq(const GradGroup<CAP>& grp, int b, int blocks, int tid,
+                                            double (&acc)[4]) {
     const int chunks = grp.chunk_prefix[grp.count];
     for (int ch = b; ch < chunks; ch += blocks) {
         const int t = grad_tensor_of(grp, ch);
         const int64_t first = (int64_t)(ch - grp.chunk_prefix[t]) * kGradUnits;
-        if (grp.bf16[t])
-            chunk_sumsq<true>(grp.g[t], grp.rows[t], grp.cols[t], grp.ld_g[t], first, acc);
-        else
-            chunk_sumsq<false>(grp.g[t], grp.rows[t], grp.cols[t], grp.ld_g[t], first, acc);
+        const int64_t rows = grp.rows[t], cols = grp.cols[t], ld = grp.ld_g[t];
+        const bool bf = grp.bf16[t];
+        if (whole(rows, cols, bf ? 8 : 4, first)) {
+            if (bf)
+                chunk_sumsq<true, true>(grp.g[t], rows, cols, ld, first, tid, acc);
+            else
+                chunk_sumsq<false, true>(grp.g[t], rows, cols, ld, first, tid, acc);
+        } else {
+            if (bf)
+                chunk_sumsq<true, false>(grp.g[t], rows, cols, ld, first, tid, acc);
+            else
+                chunk_sumsq<false, false>(grp.g[t], rows, cols, ld, first, tid, acc);
+        }
     }
 }
 
 // The chunks in the order opposite to the sum's: what it read last is the
 // likeliest to be left in the memory-side cache.
 template <int CAP>
-__device__ __forceinline__ void group_scale(const GradGroup<CAP>& grp, int b, int blocks, float scale) {
+__device__ __forceinline__ void group_scale(const GradGroup<CAP>& grp, int b, int blocks, int tid, float scale) {
     const int chunks = grp.chunk_prefix[grp.count];
     for (int k = b; k < chunks; k += blocks) {
         const int ch = chunks - 1 - k;
@@ -206,16 +242,17 @@ __device__ __forceinline__ void group_scale(const GradGroup<CAP>& grp, int b, in
         if (scale == 1.f && grp.out[t] == grp.g[t]) continue;
         const int64_t first = (int64_t)(ch - grp.chunk_prefix[t]) * kGradUnits;
         const int64_t rows = grp.rows[t], cols = grp.cols[t], lg = grp.ld_g[t], lo = grp.ld_out[t];
+        const bool full = whole(rows, cols, grp.bf16[t] ? 8 : 4, first);
+        auto go = [&](auto bf, auto obf) {
+            if (full)
+                chunk_scale<bf, obf, true>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, tid, scale);
+            else
+                chunk_scale<bf, obf, false>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, tid, scale);
+        };
         if (grp.bf16[t]) {
-            if (grp.out_bf16[t])
-                chunk_scale<true, true>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
-            else
-                chunk_scale<true, false>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
+            if (grp.out_bf16[t]) go(std::true_type{}, std::true_type{}); else go(std::true_type{}, std::false_type{});
         } else {
-            if (grp.out_bf16[t])
-                chunk_scale<false, true>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
-            else
-                chunk_scale<false, false>(grp.g[t], grp.out[t], rows, cols, lg, lo, first, scale);
+            if (grp.out_bf16[t]) go(std::false_type{}, std::true_type{}); else go(std::false_type{}, std::false_type{});
         }
     }
 }
@@ -256,7 +293,7 @@ __global__ __launch_bounds__(256) void grad_sumsq_kernel(GradGroup<CAP> grp, int
                                                          double* partials) {
     __shared__ double red[4];
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    group_sumsq(grp, blockIdx.x, blocks, acc);
+    group_sumsq(grp, blockIdx.x, blocks, threadIdx.x, acc);
     const double tot = block_sum<256>((acc[0] + acc[1]) + (acc[2] + acc[3]), red);
     if (threadIdx.x == 0) gst(partials + blockIdx.x, tot);
 }
@@ -277,19 +314,23 @@ __global__ __launch_bounds__(256) void grad_scale_kernel(GradGroup<CAP> grp, int
     __shared__ double red[4];
     const double s = partials_sum<256>(partials, n, red);
     const float scale = clip_scale(s, max_norm, norm_out, scale_out, blockIdx.x == 0 && threadIdx.x == 0);
-    group_scale(grp, blockIdx.x, blocks, scale);
+    group_scale(grp, blockIdx.x, blocks, threadIdx.x, scale);
 }
 
+// Everything by one workgroup; each 256 of its threads take a chunk.
+constexpr int kSingleThreads = 1024;
+
 template <int CAP>
-__global__ __launch_bounds__(256) void grad_single_kernel(GradGroup<CAP> grp, int clip, float max_norm,
-                                                          float* norm_out, float* scale_out) {
-    __shared__ double red[4];
+__global__ __launch_bounds__(kSingleThreads) void grad_single_kernel(GradGroup<CAP> grp, int clip, float max_norm,
+                                                                     float* norm_out, float* scale_out) {
+    __shared__ double red[kSingleThreads / 64];
+    const int team = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8), tid = threadIdx.x & 255;
     double acc[4] = {0.0, 0.0, 0.0, 0.0};
-    group_sumsq(grp, 0, 1, acc);
+    group_sumsq(grp, team, kSingleThreads / 256, tid, acc);
     // the barrier within also keeps the outputs behind every read of the sum
-    const double s = block_sum<256>((acc[0] + acc[1]) + (acc[2] + acc[3]), red);
+    const double s = block_sum<kSingleThreads>((acc[0] + acc[1]) + (acc[2] + acc[3]), red);
     const float scale = clip_scale(s, max_norm, norm_out, scale_out, threadIdx.x == 0);
-    if (clip) group_scale(grp, 0, 1, scale);
+    if (clip) group_scale(grp, team, kSingleThreads / 256, tid, scale);
 }
 
 }  // namespace
@@ -316,7 +357,7 @@ hipError_t launch_grad_scale(const GradGroup<CAP>& g, int blocks, const double* 
 template <int CAP>
 hipError_t launch_grad_single(const GradGroup<CAP>& g, int clip, float max_norm, float* norm_out,
                               float* scale_out, hipStream_t st) {
-    grad_single_kernel<CAP><<<1, 256, 0, st>>>(g, clip, max_norm, norm_out, scale_out);
+    grad_single_kernel<CAP><<<1, kSingleThreads, 0, st>>>(g, clip, max_norm, norm_out, scale_out);
     return hipGetLastError();
 }
 
