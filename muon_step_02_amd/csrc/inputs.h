@@ -99,6 +99,7 @@ struct SmaxCall {
     float scale;
     int32_t tile;            // queries of a tile
     int32_t qtiles, splits;  // bound of query tiles over all sequences, key parts of each
+    int32_t tile_major;      // order of the workgroups: a tile's heads together
 };
 constexpr int kSmaxTile = 64;   // queries (and keys) per tile of the kernel for any type
 constexpr int kSmaxLong = 512;  // mean queries of a sequence from which tiles hold 256
