@@ -335,6 +335,44 @@ __device__ __forceinline__ void for_each_chunk(const f32x16 (&acc)[C::FM][C::FN]
     __syncthreads();
 }
 
+// The tile by waves, without a barrier: each wave passes its own rows through
+// `mine` (16 x TN floats of LDS), 16 rows at a time, and gets them back four
+// columns a lane, a row's TN columns side by side.  put(b, q, row, column,
+// values) for piece q of band b; ahead(b) as for for_each_chunk.
+template <class C>
+constexpr int wave_pieces() { return 16 * C::TN / 256; }
+template <class C>
+__device__ __forceinline__ int wave_row(int b, int q) {
+    return (threadIdx.x >> 6) / C::WN * C::TM + b * 16 + (q * 64 + (threadIdx.x & 63)) / (C::TN / 4);
+}
+template <class C>
+__device__ __forceinline__ int wave_col() {
+    return (threadIdx.x >> 6) % C::WN * C::TN + (threadIdx.x & 63) % (C::TN / 4) * 4;
+}
+template <class C, class A, class F>
+__device__ __forceinline__ void for_each_piece(const f32x16 (&acc)[C::FM][C::FN], float* mine, A&& ahead, F&& put) {
+    static_assert(64 % (C::TN / 4) == 0, "a piece is whole rows");
+    const int lane = threadIdx.x & 63;
+    // rows r and r + 4 of a store lie 32 banks apart
+    auto at = [](int r, int c) { return r * C::TN + (c ^ ((r & 4) << 3)); };
+#pragma unroll
+    for (int b = 0; b < C::TM / 16; ++b) {
+        ahead(b);
+        // the wave's own earlier reads of `mine` are done: LDS is in order
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                mine[at(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3), j * 32 + (lane & 31))] = acc[b / 2][j][b % 2 * 8 + r];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int q = 0; q < wave_pieces<C>(); ++q)
+            put(b, q, wave_row<C>(b, q), wave_col<C>(),
+                *reinterpret_cast<const float4*>(mine + at((q * 64 + lane) / (C::TN / 4), lane % (C::TN / 4) * 4)));
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 __device__ __forceinline__ uint4 pack8(const float* v) {
     uint4 o;
     o.x = (uint32_t)f32_to_bf16_bits(v[0]) | ((uint32_t)f32_to_bf16_bits(v[1]) << 16);
