@@ -66,34 +66,27 @@ __device__ __forceinline__ bool find_group(const ExpertCall& c, int mt, Group& g
     return false;
 }
 
-__device__ __forceinline__ const void* at(const void* base, int bf16, int64_t off) {
-    return reinterpret_cast<const char*>(base) + off * (bf16 ? 2 : 4);
-}
+// ---- fp32 of any alignment and size: 64 x 64 tiles -------------------------
 
-// ---- any type, alignment and size: 64 x 64 tiles in fp32 -------------------
-
-// One value of the result: rounded once, from the fp32 sum.
-__device__ __forceinline__ void put_value(void* base, int bf16, int64_t off, float v, int accumulate) {
-    if (bf16) {
-        uint16_t* p = reinterpret_cast<uint16_t*>(base) + off;
-        if (accumulate) v += bf16_bits_to_f32(gld(p));
-        gst(p, f32_to_bf16_bits(v));
-    } else {
-        float* p = reinterpret_cast<float*>(base) + off;
-        if (accumulate) v += gld(p);
-        gst(p, v);
-    }
-}
-
-__device__ __forceinline__ void put_tile(const any::f32x16& acc, void* base, int bf16, int64_t ld,
-                                         int rows, int cols, int accumulate) {
+// A tile of the result, one value at a time: rounded once, from the fp32 sum.
+// Old values are loaded all before the first store: a load behind a store
+// would wait for it.
+__device__ __forceinline__ void put_tile(const any::f32x16& acc, float* out, int64_t ld, int rows, int cols,
+                                         int accumulate) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int j = 32 * (wave & 1) + (lane & 31);
-    if (j >= cols) return;
+    const int col = 32 * (wave & 1) + (lane & 31), row0 = 32 * (wave >> 1) + 4 * (lane >> 5);
+    if (col >= cols) return;
+    float v[16];
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-        const int i = 32 * (wave >> 1) + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        if (i < rows) put_value(base, bf16, (int64_t)i * ld + j, acc[r], accumulate);
+        const int row = row0 + 8 * (r >> 2) + (r & 3);
+        v[r] = acc[r];
+        if (accumulate && row < rows) v[r] += gld(out + (int64_t)row * ld + col);
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+        const int row = row0 + 8 * (r >> 2) + (r & 3);
+        if (row < rows) gst(out + (int64_t)row * ld + col, v[r]);
     }
 }
 
@@ -109,12 +102,11 @@ __global__ __launch_bounds__(256) void expert_rows_any_kernel(ExpertCall c, Expe
     const int N = OP == kExpertForward ? c.rows : c.cols;
     const int K = OP == kExpertForward ? c.cols : c.rows;
     const int nrows = min(any::kTile, g.row1 - i0), ncols = min(any::kTile, N - j0);
-    const any::Operand p{at(c.a, c.bf16, (int64_t)i0 * c.ld_a), c.ld_a, nrows};
-    const void* we = w.w[g.e];
-    const any::Operand q{at(we, c.bf16, OP == kExpertForward ? (int64_t)j0 * c.ld_w : j0), c.ld_w, ncols};
-    const any::f32x16 acc = any::product<false, OP == kExpertGradInput>(p, q, c.bf16, K, lds);
-    void* out = const_cast<void*>(at(c.c, c.bf16, (int64_t)i0 * c.ld_c + j0));
-    put_tile(acc, out, c.bf16, c.ld_c, nrows, ncols, 0);
+    const any::Operand p{reinterpret_cast<const float*>(c.a) + (int64_t)i0 * c.ld_a, c.ld_a, nrows};
+    const float* we = reinterpret_cast<const float*>(w.w[g.e]);
+    const any::Operand q{we + (OP == kExpertForward ? (int64_t)j0 * c.ld_w : j0), c.ld_w, ncols};
+    const any::f32x16 acc = any::product<false, OP == kExpertGradInput>(p, q, 0, K, lds);
+    put_tile(acc, reinterpret_cast<float*>(c.c) + (int64_t)i0 * c.ld_c + j0, c.ld_c, nrows, ncols, 0);
 }
 
 // Weight gradient: block -> (expert, row tile, column tile) of dW.
@@ -130,11 +122,10 @@ __global__ __launch_bounds__(256) void expert_weight_any_kernel(ExpertCall c, Ex
     if (c.accumulate && r1 == r0) return;
     const int i0 = mt * any::kTile, j0 = nt * any::kTile;
     const int nrows = min(any::kTile, c.rows - i0), ncols = min(any::kTile, c.cols - j0);
-    const any::Operand p{at(c.b, c.bf16, (int64_t)r0 * c.ld_b + i0), c.ld_b, nrows};
-    const any::Operand q{at(c.a, c.bf16, (int64_t)r0 * c.ld_a + j0), c.ld_a, ncols};
-    const any::f32x16 acc = any::product<true, true>(p, q, c.bf16, r1 - r0, lds);
-    void* out = const_cast<void*>(at(w.w[e], c.out_bf16, (int64_t)i0 * c.ld_w + j0));
-    put_tile(acc, out, c.out_bf16, c.ld_w, nrows, ncols, c.accumulate);
+    const any::Operand p{reinterpret_cast<const float*>(c.b) + (int64_t)r0 * c.ld_b + i0, c.ld_b, nrows};
+    const any::Operand q{reinterpret_cast<const float*>(c.a) + (int64_t)r0 * c.ld_a + j0, c.ld_a, ncols};
+    const any::f32x16 acc = any::product<true, true>(p, q, 0, r1 - r0, lds);
+    put_tile(acc, reinterpret_cast<float*>(w.w[e]) + (int64_t)i0 * c.ld_w + j0, c.ld_w, nrows, ncols, c.accumulate);
 }
 
 // ---- bf16 on the matrix cores ------------------------------------------------
@@ -290,6 +281,94 @@ __global__ __launch_bounds__(128) void expert_few_kernel(ExpertCall c, ExpertPtr
     rows_product<bf::Cfg<kFewM, kFewN, 1, 2, false, OP == kExpertGradInput, 64, 4>>(c, t, st);
 }
 
+// Four values of a result, or as many as its row still holds, at the alignment
+// of 16 (8) bytes or, LOOSE, of one value.
+template <bool LOOSE>
+__device__ __forceinline__ float4 load4(const float* p, int left) {
+    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+    if (!LOOSE) return gld(reinterpret_cast<const float4*>(p));
+    if (left >= 4) {
+        const f4 v = *(const MUON_GLOBAL f4*)p;
+        return make_float4(v.x, v.y, v.z, v.w);
+    }
+    return make_float4(left > 0 ? gld(p) : 0.f, left > 1 ? gld(p + 1) : 0.f, left > 2 ? gld(p + 2) : 0.f, 0.f);
+}
+template <bool LOOSE>
+__device__ __forceinline__ float4 load4(const uint16_t* p, int left) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
+    uint2 w = make_uint2(0, 0);
+    if (!LOOSE) {
+        w = gld(reinterpret_cast<const uint2*>(p));
+    } else if (left >= 4) {
+        const u2 v = *(const MUON_GLOBAL u2*)p;
+        w = make_uint2(v.x, v.y);
+    } else {
+        if (left > 0) w.x = gld(p);
+        if (left > 1) w.x |= (uint32_t)gld(p + 1) << 16;
+        if (left > 2) w.y = gld(p + 2);
+    }
+    return make_float4(bf16_bits_to_f32(w.x & 0xffff), bf16_bits_to_f32(w.x >> 16), bf16_bits_to_f32(w.y & 0xffff),
+                       bf16_bits_to_f32(w.y >> 16));
+}
+template <bool LOOSE>
+__device__ __forceinline__ void store4(float* p, int left, const float4& v) {
+    typedef float f4 __attribute__((ext_vector_type(4), aligned(4)));
+    if (!LOOSE) {
+        if (left > 0) gst(reinterpret_cast<float4*>(p), v);
+    } else if (left >= 4) {
+        *(MUON_GLOBAL f4*)p = f4{v.x, v.y, v.z, v.w};
+    } else {
+        if (left > 0) gst(p, v.x);
+        if (left > 1) gst(p + 1, v.y);
+        if (left > 2) gst(p + 2, v.z);
+    }
+}
+template <bool LOOSE>
+__device__ __forceinline__ void store4(uint16_t* p, int left, const float4& v) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(2)));
+    const uint16_t a = f32_to_bf16_bits(v.x), b = f32_to_bf16_bits(v.y), c = f32_to_bf16_bits(v.z),
+                   d = f32_to_bf16_bits(v.w);
+    const uint2 w = make_uint2(a | (uint32_t)b << 16, c | (uint32_t)d << 16);
+    if (!LOOSE) {
+        if (left > 0) gst(reinterpret_cast<uint2*>(p), w);
+    } else if (left >= 4) {
+        *(MUON_GLOBAL u2*)p = u2{w.x, w.y};
+    } else {
+        if (left > 0) gst(p, a);
+        if (left > 1) gst(p + 1, b);
+        if (left > 2) gst(p + 2, c);
+    }
+}
+
+// The tile at `out`, rounded once, or added to what it holds: old values are
+// loaded one band ahead.  mine: the wave's 16 x TN floats of LDS.
+template <class C, class T, bool ADD, bool LOOSE>
+__device__ __forceinline__ void store_result(const bf::f32x16 (&acc)[C::FM][C::FN], float* mine, T* out, int64_t ld,
+                                             int rows, int cols) {
+    constexpr int P = bf::wave_pieces<C>();
+    float4 old[2][P];
+    const int col = bf::wave_col<C>();
+    auto load_old = [&](int b) {
+        if constexpr (ADD) {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                // behind the last row (and, not LOOSE, column): any value in range
+                const int r = min(bf::wave_row<C>(b, i), rows - 1);
+                old[b & 1][i] = load4<LOOSE>(out + r * ld + (LOOSE ? col : min(col, cols - 4)), cols - col);
+            }
+        }
+    };
+    load_old(0);
+    bf::for_each_piece<C>(acc, mine, [&](int b) { if (b + 1 < C::TM / 16) load_old(b + 1); },
+                          [&](int b, int i, int r, int, float4 v) {
+        if constexpr (ADD) {
+            const float4& o = old[b & 1][i];
+            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+        if (r < rows) store4<LOOSE>(out + r * ld + col, cols - col, v);
+    });
+}
+
 // Weight gradient on 128 x 256 tiles of four waves, two workgroups a compute
 // unit: a group's rows are a short K, so reading and writing dW is most of
 // the traffic, and one workgroup does it while the other multiplies.  With
@@ -321,61 +400,20 @@ __global__ __launch_bounds__(256, 2) void expert_weight_kernel(ExpertCall c, Exp
                         2 * ((int64_t)(K - 1) * c.ld_b + c.rows - i0)};
     const bf::Operand q{reinterpret_cast<const uint16_t*>(c.a) + (int64_t)r0 * c.ld_a + j0, c.ld_a,
                         2 * ((int64_t)(K - 1) * c.ld_a + c.cols - j0)};
-    const int64_t ld = c.ld_w;
     using T = typename std::conditional<OBF, uint16_t, float>::type;
-    T* const out = reinterpret_cast<T*>(w.w[e]) + (int64_t)i0 * ld + j0;
     bf::f32x16 acc[C::FM][C::FN];
     bf::zero<C>(acc);
     bf::product<C>(acc, p, q, K, st);
     __syncthreads();  // every wave has read its last fragments
-    using W = typename std::conditional<OBF, uint2, uint4>::type;  // four values
-    constexpr int P = bf::wave_pieces<C>();
-    W old[2][P];
-    const int col = bf::wave_col<C>();
-    auto load_old = [&](int b) {
-        if constexpr (ADD) {
-#pragma unroll
-            for (int i = 0; i < P; ++i) {
-                // behind the last row or column: any value in range
-                const int r = min(bf::wave_row<C>(b, i), rows - 1);
-                old[b & 1][i] = gld(reinterpret_cast<const W*>(out + r * ld + min(col, cols - 4)));
-            }
-        }
-    };
-    load_old(0);
     const int wave = threadIdx.x >> 6;
-    constexpr int MINE = 16 * C::TN;
-    float* const mine = reinterpret_cast<float*>(wave < 2 ? lq0 : lq1) + wave % 2 * MINE;
-    bf::for_each_piece<C>(acc, mine, [&](int b) { if (b + 1 < C::TM / 16) load_old(b + 1); },
-                          [&](int b, int i, int r, int, float4 v) {
-        T* const o = out + r * ld + col;
-        const W w = old[b & 1][i];
-        if constexpr (OBF) {
-            if constexpr (ADD) {
-                v.x += __builtin_bit_cast(float, w.x << 16);
-                v.y += __builtin_bit_cast(float, w.x & 0xffff0000u);
-                v.z += __builtin_bit_cast(float, w.y << 16);
-                v.w += __builtin_bit_cast(float, w.y & 0xffff0000u);
-            }
-            const uint2 u = make_uint2((uint32_t)f32_to_bf16_bits(v.x) | (uint32_t)f32_to_bf16_bits(v.y) << 16,
-                                       (uint32_t)f32_to_bf16_bits(v.z) | (uint32_t)f32_to_bf16_bits(v.w) << 16);
-            if (r < rows && col < cols) gst(reinterpret_cast<uint2*>(o), u);
-        } else {
-            if constexpr (ADD) {
-                v.x += __builtin_bit_cast(float, w.x);
-                v.y += __builtin_bit_cast(float, w.y);
-                v.z += __builtin_bit_cast(float, w.z);
-                v.w += __builtin_bit_cast(float, w.w);
-            }
-            if (r < rows && col < cols) gst(reinterpret_cast<float4*>(o), v);
-        }
-    });
+    store_result<C, T, ADD, false>(acc, reinterpret_cast<float*>(wave < 2 ? lq0 : lq1) + wave % 2 * 16 * C::TN,
+                                   reinterpret_cast<T*>(w.w[e]) + (int64_t)i0 * c.ld_w + j0, c.ld_w, rows, cols);
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // bf16 operands whose rows all start on 16 bytes and hold whole 16-byte
-// chunks; anything else takes the 64 x 64 tiles.
+// chunks: copied to LDS as they are.  Others go through registers.
 bool chunked(ExpertOp op, const ExpertCall& c, const void* const* w) {
     if (!c.bf16 || c.rows % 8 || c.cols % 8 || c.ld_a % 8 || c.ld_w % 8 || !aligned16(c.a)) return false;
     if (op == kExpertGradWeight ? (c.ld_b % 8 || !aligned16(c.b)) : (c.ld_c % 8 || !aligned16(c.c))) return false;
@@ -447,20 +485,97 @@ hipError_t launch_bf16(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& 
     return hipGetLastError();
 }
 
+// ---- bf16 of any alignment and size -------------------------------------------
+
+// T x T tiles of four waves through registers; blocks as in the kernels for
+// any type.
+template <ExpertOp OP, int T, int CAP>
+__global__ __launch_bounds__(256) void expert_rows_loose_kernel(ExpertCall c, ExpertPtrs<CAP> w, int ntiles) {
+    constexpr bool QKM = OP == kExpertGradInput;
+    using C = bf::Cfg<T, T, 2, 2, false, QKM>;
+    __shared__ __attribute__((aligned(1024))) uint16_t l0[T * 64], l1[T * 64], l2[T * 64], l3[T * 64];
+    const bf::Stages<2> st{{l0, l2}, {l1, l3}};
+    const int mt = blockIdx.x / ntiles, nt = blockIdx.x - mt * ntiles;
+    Group g;
+    if (!find_group<T>(c, mt, g)) return;
+    const int i0 = g.row0 + g.tile * T, j0 = nt * T;
+    const int N = QKM ? c.cols : c.rows, K = QKM ? c.rows : c.cols;
+    const int rows = min(T, g.row1 - i0), cols = min(T, N - j0);
+    const uint16_t* we = reinterpret_cast<const uint16_t*>(w.w[g.e]);
+    const bf::AnyOperand p{reinterpret_cast<const uint16_t*>(c.a) + (int64_t)i0 * c.ld_a, c.ld_a, rows};
+    const bf::AnyOperand q{we + (QKM ? j0 : (int64_t)j0 * c.ld_w), c.ld_w, cols};
+    bf::f32x16 acc[C::FM][C::FN];
+    bf::zero<C>(acc);
+    bf::product_any<C>(acc, p, q, K, st);
+    store_result<C, uint16_t, false, true>(acc, reinterpret_cast<float*>(l0) + (threadIdx.x >> 6) * 16 * C::TN,
+                                           reinterpret_cast<uint16_t*>(c.c) + (int64_t)i0 * c.ld_c + j0, c.ld_c, rows,
+                                           cols);
+}
+
+template <int T, int CAP, bool OBF, bool ADD>
+__global__ __launch_bounds__(256) void expert_weight_loose_kernel(ExpertCall c, ExpertPtrs<CAP> w, int mtiles, int ntiles) {
+    using C = bf::Cfg<T, T, 2, 2, true, true>;
+    __shared__ __attribute__((aligned(1024))) uint16_t l0[T * 64], l1[T * 64], l2[T * 64], l3[T * 64];
+    const bf::Stages<2> st{{l0, l2}, {l1, l3}};
+    const int per = mtiles * ntiles;
+    const int e = blockIdx.x / per, rest = blockIdx.x - e * per;
+    const int mt = rest / ntiles, nt = rest - mt * ntiles;
+    int r0, r1;
+    group_rows(c, e, r0, r1);
+    if (ADD && r1 == r0) return;
+    const int i0 = mt * T, j0 = nt * T;
+    const int rows = min(T, c.rows - i0), cols = min(T, c.cols - j0);
+    const bf::AnyOperand p{reinterpret_cast<const uint16_t*>(c.b) + (int64_t)r0 * c.ld_b + i0, c.ld_b, rows};
+    const bf::AnyOperand q{reinterpret_cast<const uint16_t*>(c.a) + (int64_t)r0 * c.ld_a + j0, c.ld_a, cols};
+    bf::f32x16 acc[C::FM][C::FN];
+    bf::zero<C>(acc);
+    bf::product_any<C>(acc, p, q, r1 - r0, st);
+    using O = typename std::conditional<OBF, uint16_t, float>::type;
+    store_result<C, O, ADD, true>(acc, reinterpret_cast<float*>(l0) + (threadIdx.x >> 6) * 16 * C::TN,
+                                  reinterpret_cast<O*>(w.w[e]) + (int64_t)i0 * c.ld_w + j0, c.ld_w, rows, cols);
+}
+
+template <int T, int CAP>
+hipError_t launch_loose(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& w, hipStream_t st) {
+    const int64_t nr = (c.rows + T - 1) / T, nc = (c.cols + T - 1) / T;
+    const int64_t mt = c.tokens / T + (c.tokens < c.experts ? c.tokens : c.experts);
+    if (op == kExpertGradWeight) {
+        const unsigned n = (unsigned)(c.experts * nr * nc);
+        if (c.out_bf16) {
+            if (c.accumulate)
+                expert_weight_loose_kernel<T, CAP, true, true><<<n, 256, 0, st>>>(c, w, (int)nr, (int)nc);
+            else
+                expert_weight_loose_kernel<T, CAP, true, false><<<n, 256, 0, st>>>(c, w, (int)nr, (int)nc);
+        } else {
+            if (c.accumulate)
+                expert_weight_loose_kernel<T, CAP, false, true><<<n, 256, 0, st>>>(c, w, (int)nr, (int)nc);
+            else
+                expert_weight_loose_kernel<T, CAP, false, false><<<n, 256, 0, st>>>(c, w, (int)nr, (int)nc);
+        }
+    } else if (op == kExpertForward)
+        expert_rows_loose_kernel<kExpertForward, T, CAP><<<(unsigned)(mt * nr), 256, 0, st>>>(c, w, (int)nr);
+    else
+        expert_rows_loose_kernel<kExpertGradInput, T, CAP><<<(unsigned)(mt * nc), 256, 0, st>>>(c, w, (int)nc);
+    return hipGetLastError();
+}
+
 template <int CAP>
 hipError_t launch_any(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& w, hipStream_t st) {
     const int T = any::kTile;
     const int64_t nr = (c.rows + T - 1) / T, nc = (c.cols + T - 1) / T;
-    if (op == kExpertGradWeight) {
-        expert_weight_any_kernel<CAP><<<(unsigned)(c.experts * nr * nc), 256, 0, st>>>(c, w, (int)nr, (int)nc);
-    } else {
-        // at most this many row tiles: every group may end in a ragged one
-        const int64_t mt = c.tokens / T + (c.tokens < c.experts ? c.tokens : c.experts);
-        if (op == kExpertForward)
-            expert_rows_any_kernel<kExpertForward, CAP><<<(unsigned)(mt * nr), 256, 0, st>>>(c, w, (int)nr);
-        else
-            expert_rows_any_kernel<kExpertGradInput, CAP><<<(unsigned)(mt * nc), 256, 0, st>>>(c, w, (int)nc);
+    // at most this many row tiles: every group may end in a ragged one
+    const int64_t mt = c.tokens / T + (c.tokens < c.experts ? c.tokens : c.experts);
+    if (c.bf16) {
+        // 128 x 128 tiles where they fill the chip twice
+        const int64_t tiles = op == kExpertGradWeight ? c.experts * nr * nc : mt * (op == kExpertForward ? nr : nc);
+        return tiles >= 4 * 1024 ? launch_loose<128, CAP>(op, c, w, st) : launch_loose<64, CAP>(op, c, w, st);
     }
+    if (op == kExpertGradWeight)
+        expert_weight_any_kernel<CAP><<<(unsigned)(c.experts * nr * nc), 256, 0, st>>>(c, w, (int)nr, (int)nc);
+    else if (op == kExpertForward)
+        expert_rows_any_kernel<kExpertForward, CAP><<<(unsigned)(mt * nr), 256, 0, st>>>(c, w, (int)nr);
+    else
+        expert_rows_any_kernel<kExpertGradInput, CAP><<<(unsigned)(mt * nc), 256, 0, st>>>(c, w, (int)nc);
     return hipGetLastError();
 }
 

@@ -1,7 +1,7 @@
 // A 64 x 64 product tile in fp32 for operands of any type, alignment, leading
 // dimension and size (gfx950): C[i][j] = sum_k P[i][k] Q[j][k].
 //
-// Slabs of 16 k are read into registers (16 bytes a thread where the row
+// Slabs of 32 k are read into registers (16 bytes a thread where the row
 // allows it, whatever its alignment), widened to fp32 and laid out k-major in
 // LDS; four waves hold a 32 x 32 block each and run v_mfma_f32_32x32x2f32.
 // One such instruction keeps a SIMD busy for 64 cycles and needs two 4-byte
@@ -19,7 +19,8 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint16_t u16x4u __attribute__((ext_vector_type(4), aligned(2)));
 
 constexpr int kTile = 64;
-constexpr int kBK = 16;
+constexpr int kBK = 32;  // 64: LDS for two workgroups a compute unit only, 90 -> 62 TFLOP/s
+constexpr int kF = kTile * kBK / 1024;  // 4-value loads of a thread, operand and slab
 constexpr int kLd = 68;  // LDS row of 64 values, padded
 
 struct Lds {
@@ -58,29 +59,29 @@ __device__ __forceinline__ float4 load4_any(const void* base, int bf16, int64_t 
     return r;
 }
 
-// Thread t's four values of the slab at k0: row t / 4, k 4 (t % 4) ... + 3,
-// or with KM rows 4 (t % 16) ... + 3 of k t / 16.
+// Load f of thread t for the slab at k0: row t / 8 + 32 f, k 4 (t % 8) ... + 3,
+// or with KM rows 4 (t % 16) ... + 3 of k t / 16 + 16 f.
 template <bool KM>
-__device__ __forceinline__ float4 fetch(const Operand& o, int bf16, int64_t k0, int64_t K) {
+__device__ __forceinline__ float4 fetch(const Operand& o, int bf16, int64_t k0, int64_t K, int f) {
     const int t = threadIdx.x;
     if (KM) {
-        const int64_t k = k0 + (t >> 4);
+        const int64_t k = k0 + (t >> 4) + 16 * f;
         const int i = (t & 15) * 4;
         return load4_any(o.base, bf16, k * o.ld + i, k < K ? o.n - i : 0);
     }
-    const int i = t >> 2;
-    const int64_t k = k0 + (t & 3) * 4;
+    const int i = (t >> 3) + 32 * f;
+    const int64_t k = k0 + (t & 7) * 4;
     const int64_t left = K - k;
     return load4_any(o.base, bf16, (int64_t)i * o.ld + k, i < o.n ? (left > 4 ? 4 : (int)left) : 0);
 }
 
 template <bool KM>
-__device__ __forceinline__ void put(float* s, const float4& v) {
+__device__ __forceinline__ void put(float* s, const float4& v, int f) {
     const int t = threadIdx.x;
     if (KM) {
-        *reinterpret_cast<float4*>(s + (t >> 4) * kLd + (t & 15) * 4) = v;
+        *reinterpret_cast<float4*>(s + ((t >> 4) + 16 * f) * kLd + (t & 15) * 4) = v;
     } else {
-        float* d = s + (t & 3) * 4 * kLd + (t >> 2);
+        float* d = s + (t & 7) * 4 * kLd + (t >> 3) + 32 * f;
         d[0] = v.x;
         d[kLd] = v.y;
         d[2 * kLd] = v.z;
@@ -101,16 +102,27 @@ __device__ __forceinline__ f32x16 product(const Operand& p, const Operand& q, in
     for (int r = 0; r < 16; ++r) acc[r] = 0.f;
     if (K <= 0) return acc;
     __syncthreads();  // a previous tile's reads are done
-    put<PKM>(s.p[0], fetch<PKM>(p, bf16, 0, K));
-    put<QKM>(s.q[0], fetch<QKM>(q, bf16, 0, K));
+    float4 np[kF], nq[kF];
+#pragma unroll
+    for (int f = 0; f < kF; ++f) {
+        np[f] = fetch<PKM>(p, bf16, 0, K, f);
+        nq[f] = fetch<QKM>(q, bf16, 0, K, f);
+    }
+#pragma unroll
+    for (int f = 0; f < kF; ++f) {
+        put<PKM>(s.p[0], np[f], f);
+        put<QKM>(s.q[0], nq[f], f);
+    }
     __syncthreads();
     int cur = 0;
     for (int64_t k0 = 0; k0 < K; k0 += kBK) {
         const bool more = k0 + kBK < K;
-        float4 np = make_float4(0.f, 0.f, 0.f, 0.f), nq = np;
         if (more) {
-            np = fetch<PKM>(p, bf16, k0 + kBK, K);
-            nq = fetch<QKM>(q, bf16, k0 + kBK, K);
+#pragma unroll
+            for (int f = 0; f < kF; ++f) {
+                np[f] = fetch<PKM>(p, bf16, k0 + kBK, K, f);
+                nq[f] = fetch<QKM>(q, bf16, k0 + kBK, K, f);
+            }
         }
         const float* sp = s.p[cur] + (lane >> 5) * kLd + pi;
         const float* sq = s.q[cur] + (lane >> 5) * kLd + qi;
@@ -118,8 +130,11 @@ __device__ __forceinline__ f32x16 product(const Operand& p, const Operand& q, in
         for (int k = 0; k < kBK; k += 2)
             acc = __builtin_amdgcn_mfma_f32_32x32x2f32(sp[k * kLd], sq[k * kLd], acc, 0, 0, 0);
         if (more) {
-            put<PKM>(s.p[cur ^ 1], np);
-            put<QKM>(s.q[cur ^ 1], nq);
+#pragma unroll
+            for (int f = 0; f < kF; ++f) {
+                put<PKM>(s.p[cur ^ 1], np[f], f);
+                put<QKM>(s.q[cur ^ 1], nq[f], f);
+            }
         }
         __syncthreads();
         cur ^= 1;

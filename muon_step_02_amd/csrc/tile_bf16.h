@@ -276,6 +276,100 @@ __device__ __forceinline__ void product(f32x16 (&acc)[C::FM][C::FN], const Opera
     wait_vmcnt<0>();
 }
 
+// ---- operands of any alignment ----------------------------------------------
+// The same slabs through registers: a chunk of 8 bf16 at any address (one
+// 16-byte load where the row holds it whole, single values at its end), then
+// a 16-byte write to its place in the slab.
+
+// 16 bytes at the alignment of a bf16: gfx950 allows unaligned global accesses.
+typedef uint32_t u32x4h __attribute__((ext_vector_type(4), aligned(2)));
+__device__ __forceinline__ uint4 chunk_any(const uint16_t* p, int64_t left) {
+    if (left >= 8) {
+        const u32x4h u = *(const MUON_GLOBAL u32x4h*)p;
+        return make_uint4(u.x, u.y, u.z, u.w);
+    }
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        if (e < left) w[e >> 1] |= (uint32_t)gld(p + e) << 16 * (e & 1);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// rows x K of an operand stored K-contiguous, K x cols of one stored k-major.
+struct AnyOperand {
+    const uint16_t* base;
+    int64_t ld;
+    int n;  // rows, or columns
+};
+
+// Chunk f of this thread for the slab at k0, and its place in it.  R: the
+// tile's rows (columns); NT threads.
+template <int R, int NT, bool KM>
+__device__ __forceinline__ uint4 fetch_any(const AnyOperand& o, int64_t k0, int64_t K, int f) {
+    const int ch = f * NT + threadIdx.x;
+    if constexpr (KM) {
+        const int64_t k = k0 + ch / (R / 8);
+        const int c = ch % (R / 8) * 8;
+        return chunk_any(o.base + k * o.ld + c, k < K ? o.n - c : 0);
+    } else {
+        const int row = ch / 8;
+        const int64_t k = k0 + ch % 8 * 8;
+        return chunk_any(o.base + row * o.ld + k, row < o.n ? K - k : 0);
+    }
+}
+template <int R, int NT, bool KM>
+__device__ __forceinline__ void put_any(uint16_t* slab, const uint4& v, int f) {
+    const int ch = f * NT + threadIdx.x;
+    const int row = ch / (KM ? R / 8 : 8), c = ch % (KM ? R / 8 : 8);
+    *reinterpret_cast<uint4*>(slab + row * (KM ? R : 64) + ((c ^ (KM ? swzk<R>(row) : swz<64>(row))) << 3)) = v;
+}
+
+// acc += the tile over k [0, K): the registers of slab kt + 2 are loaded and
+// those of slab kt + 1 written while slab kt is multiplied.
+template <class C>
+__device__ __forceinline__ void product_any(f32x16 (&acc)[C::FM][C::FN], const AnyOperand& p, const AnyOperand& q,
+                                            int64_t K, const Stages<2>& st) {
+    static_assert(C::BK == 64, "64-deep slabs");
+    constexpr int NP = C::BM * 8 / C::NT, NQ = C::BN * 8 / C::NT;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const int KT = (int)((K + 63) / 64);
+    if (KT == 0) return;
+    uint4 rp[NP], rq[NQ];
+    auto fetch = [&](int kt) {
+#pragma unroll
+        for (int f = 0; f < NP; ++f) rp[f] = fetch_any<C::BM, C::NT, C::PKM>(p, (int64_t)kt * 64, K, f);
+#pragma unroll
+        for (int f = 0; f < NQ; ++f) rq[f] = fetch_any<C::BN, C::NT, C::QKM>(q, (int64_t)kt * 64, K, f);
+    };
+    auto put = [&](uint16_t* sp, uint16_t* sq) {
+#pragma unroll
+        for (int f = 0; f < NP; ++f) put_any<C::BM, C::NT, C::PKM>(sp, rp[f], f);
+#pragma unroll
+        for (int f = 0; f < NQ; ++f) put_any<C::BN, C::NT, C::QKM>(sq, rq[f], f);
+    };
+    fetch(0);
+    put(st.p[0], st.q[0]);
+    if (KT > 1) fetch(1);
+    __syncthreads();
+    for (int kt0 = 0; kt0 < KT; kt0 += 2) {
+        unrolled<2>([&](auto u) {
+            const int kt = kt0 + u;
+            if (kt >= KT) return;
+            Frags<C> f[2];
+            read_frags<C>(st.p[u], st.q[u], 0, wm, wn, lane, f[0]);
+            if (kt + 1 < KT) put(st.p[1 - u], st.q[1 - u]);
+            if (kt + 2 < KT) fetch(kt + 2);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                if (kk < 3) read_frags<C>(st.p[u], st.q[u], kk + 1, wm, wn, lane, f[(kk + 1) & 1]);
+                mfma_frags<C>(acc, f[kk & 1]);
+            }
+            __syncthreads();
+        });
+    }
+}
+
 // Epilogue band (RB rows in fp32, in LDS): column c of row r at
 // c ^ ((r & 4) << 3) ^ ((r >> 3) << 4), so that the two half-waves of an
 // accumulator store (rows r and r + 4) lie 32 banks apart.
@@ -353,8 +447,9 @@ template <class C, class A, class F>
 __device__ __forceinline__ void for_each_piece(const f32x16 (&acc)[C::FM][C::FN], float* mine, A&& ahead, F&& put) {
     static_assert(64 % (C::TN / 4) == 0, "a piece is whole rows");
     const int lane = threadIdx.x & 63;
-    // rows r and r + 4 of a store lie 32 banks apart
-    auto at = [](int r, int c) { return r * C::TN + (c ^ ((r & 4) << 3)); };
+    // rows r and r + 4 of a store lie 32 banks apart (a row of 32 columns is
+    // no longer than that)
+    auto at = [](int r, int c) { return r * C::TN + (C::TN >= 64 ? c ^ ((r & 4) << 3) : c); };
 #pragma unroll
     for (int b = 0; b < C::TM / 16; ++b) {
         ahead(b);
