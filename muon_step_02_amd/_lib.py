@@ -343,6 +343,7 @@ def muon_init(device=0):
     lib = load()
     h = ctypes.c_void_p()
     _check(lib.muon_init(int(device), ctypes.byref(h)), "muon_init")
+    h.device = int(device)
     return h
 
 
@@ -411,17 +412,27 @@ def adamw_step_clipped_noalloc(h, tensors, hp, max_norm, norm_out=None, stream=N
 
 def _same_device(*tensors):
     """The one CUDA device of the tensors (None among them: not given)."""
-    devices = {t.device for t in tensors if t is not None}
-    if len(devices) != 1 or next(iter(devices)).type != "cuda":
-        raise ValueError("expected tensors on one CUDA device, got %s" % sorted(map(str, devices)))
-    return devices.pop()
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError("expected tensors on one device, got %s and %s" % (dev, t.device))
+    if dev is None or dev.type != "cuda":
+        raise ValueError("expected tensors on a CUDA device, got %s" % dev)
+    return dev
 
 
-def _stream_on(stream, device):
-    """`stream`, or the current stream of the tensors' device."""
+def _stream_on(stream, device, h):
+    """`stream`, or the current stream of the tensors' device, which has to be
+    the handle's."""
+    if device.index != getattr(h, "device", device.index):
+        raise ValueError("the tensors are on %s, the handle is bound to device %d" % (device, h.device))
     if stream is None:
         import torch
-        stream = torch.cuda.current_stream(device)
+        return torch.cuda.current_stream(device.index).cuda_stream
     return _stream_ptr(stream)
 
 
@@ -454,7 +465,7 @@ def muon_step_batched_scaled(h, mats, hp, grad_scale, workspace, stream=None):
     dev = _same_device(grad_scale, workspace)
     _check(load().muon_step_batched_scaled(h, arr, len(mats), ctypes.byref(hp),
                                            _scalar(grad_scale, "grad_scale"), workspace.data_ptr(),
-                                           _nbytes(workspace), _stream_on(stream, dev)),
+                                           _nbytes(workspace), _stream_on(stream, dev, h)),
            "muon_step_batched_scaled")
 
 
@@ -463,7 +474,7 @@ def adamw_step_scaled(h, tensors, hp, grad_scale, stream=None):
     arr = (AdamwTensor * len(tensors))(*tensors)
     dev = _same_device(grad_scale)
     _check(load().adamw_step_scaled(h, arr, len(tensors), ctypes.byref(hp),
-                                    _scalar(grad_scale, "grad_scale"), _stream_on(stream, dev)),
+                                    _scalar(grad_scale, "grad_scale"), _stream_on(stream, dev, h)),
            "adamw_step_scaled")
 
 
@@ -509,7 +520,7 @@ def _grad_call(name, h, grads, max_norm, workspace, norm_out, scale_out, stream)
     dev = _same_device(workspace, norm_out, scale_out)
     _check(getattr(load(), name)(h, arr, len(arr), float(max_norm), _scalar(norm_out, "norm_out"),
                                  _scalar(scale_out, "scale_out"), workspace.data_ptr(),
-                                 _nbytes(workspace), _stream_on(stream, dev)), name)
+                                 _nbytes(workspace), _stream_on(stream, dev, h)), name)
 
 
 def muon_grad_norm(h, grads, max_norm, workspace, norm_out=None, scale_out=None, stream=None):
@@ -567,7 +578,7 @@ def _expert_rows(name, h, ex, offsets, x, y, wx, wy, stream):
     px, lx = _tokens(x, wx, "the input")
     py, ly = _tokens(y, wy, "the output")
     _check(getattr(load(), name)(h, ctypes.byref(ex), po, px, lx, py, ly, x.shape[0],
-                                 _stream_on(stream, dev)), name)
+                                 _stream_on(stream, dev, h)), name)
 
 
 def muon_expert_forward(h, ex, offsets, x, y, stream=None):
@@ -592,7 +603,7 @@ def muon_expert_grad_weight(h, grads, offsets, x, dy, accumulate=False, stream=N
     px, lx = _tokens(x, grads.cols, "x")
     pd, ldd = _tokens(dy, grads.rows, "dy")
     _check(load().muon_expert_grad_weight(h, ctypes.byref(grads), po, px, lx, pd, ldd, x.shape[0],
-                                          _dt(x), 1 if accumulate else 0, _stream_on(stream, dev)),
+                                          _dt(x), 1 if accumulate else 0, _stream_on(stream, dev, h)),
            "muon_expert_grad_weight")
 
 
@@ -641,7 +652,7 @@ def muon_qk_smax(h, q, k, cu_q, cu_k, smax_q, workspace, smax_k=None, scale=None
     _check(load().muon_qk_smax(h, ctypes.byref(qk), smax_q.data_ptr() if smax_q is not None else None,
                                smax_k.data_ptr() if smax_k is not None else None,
                                1 if accumulate else 0, workspace.data_ptr(), _nbytes(workspace),
-                               _stream_on(stream, dev)), "muon_qk_smax")
+                               _stream_on(stream, dev, h)), "muon_qk_smax")
 
 
 def muon_test_gram_bf16(h, X, A, m, n, ldx, lda, s2=1.0, stream=None):

@@ -75,8 +75,8 @@ muon_status check_grad(const muon_grad& g) {
     if (g.rows < 0 || g.cols < 0 || g.rows > lim || g.cols > lim || !valid_dtype(g.grad_dtype))
         return MUON_ERR_INVALID_ARG;
     if (g.rows > 0 && g.cols > 0 && g.cols > lim / g.rows) return MUON_ERR_INVALID_ARG;
-    if (g.ld_grad < g.cols || (g.rows > 1 && g.ld_grad > lim)) return MUON_ERR_INVALID_ARG;
-    if (g.out && (!valid_dtype(g.out_dtype) || g.ld_out < g.cols || (g.rows > 1 && g.ld_out > lim)))
+    if (g.ld_grad < g.cols || (g.rows > 1 && g.ld_grad > lim / g.rows)) return MUON_ERR_INVALID_ARG;
+    if (g.out && (!valid_dtype(g.out_dtype) || g.ld_out < g.cols || (g.rows > 1 && g.ld_out > lim / g.rows)))
         return MUON_ERR_INVALID_ARG;
     return MUON_OK;
 }
@@ -282,7 +282,8 @@ muon_status expert_rows(ExpertOp op, muon_handle h, const muon_experts* ex, cons
     st = check_tokens(x, ld_x, wx, tokens, ex->dtype);
     if (st == MUON_OK) st = check_tokens(y, ld_y, wy, tokens, ex->dtype);
     if (st != MUON_OK) return st;
-    if (!grid_fits(tokens / 16 + ex->experts, (wy + 15) / 16, 1)) return MUON_ERR_INVALID_ARG;
+    // the smallest tiles: 32 x 64
+    if (!grid_fits(tokens / 32 + ex->experts, (wy + 63) / 64, 1)) return MUON_ERR_INVALID_ARG;
     const Rect more[3] = {tokens_rect(x, tokens, wx, ld_x, ex->dtype, false),
                           tokens_rect(y, tokens, wy, ld_y, ex->dtype, true),
                           rect_of(offsets, 1, ex->experts + 1, ex->experts + 1, 4, false, 0)};

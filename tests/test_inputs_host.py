@@ -64,7 +64,8 @@ def _grad_call(lib, h, grads, clip=True, max_norm=1.0, norm=4 * BUF, scale=None,
 @pytest.mark.parametrize("clip", [False, True])
 @pytest.mark.parametrize("over", [dict(rows=-1), dict(cols=-1), dict(ld_grad=7), dict(grad_dtype=2),
                                   dict(grad=None), dict(rows=1 << 41), dict(cols=1 << 41),
-                                  dict(rows=1 << 39, cols=1 << 39, ld_grad=1 << 39)])
+                                  dict(rows=1 << 39, cols=1 << 39, ld_grad=1 << 39),
+                                  dict(rows=1 << 20, ld_grad=1 << 39)])
 def test_grad_sizes_refused(lib, handle, clip, over):
     assert _grad_call(lib, handle, [_grad(**over)], clip) == INVALID
 
@@ -118,6 +119,18 @@ def test_grad_workspace_size(lib, handle):
         assert lib.muon_grad_workspace_size(handle, arr, n, ctypes.byref(sz)) == 0
         assert sz.value % 256 == 0 and sz.value >= 8 * 2048
     assert lib.muon_grad_workspace_size(handle, arr, 0, ctypes.byref(sz)) == INVALID
+
+
+def test_the_handles_device_has_to_be_the_tensors():
+    from muon_step_02_amd import _lib
+    h = ctypes.c_void_p()
+    h.device = 0
+    with pytest.raises(ValueError):
+        _lib._stream_on(None, torch.device("cuda:1"), h)
+    with pytest.raises(ValueError):
+        _lib._same_device(torch.zeros(1), None)
+    with pytest.raises(ValueError):
+        _lib._same_device(None)
 
 
 def test_scaled_steps_need_a_scale(lib, handle):
