@@ -67,6 +67,10 @@ __device__ __forceinline__ bool find_group(const ExpertCall& c, int mt, Group& g
 }
 
 // ---- fp32 of any alignment and size: 64 x 64 tiles -------------------------
+//
+// Bound by the fp32 matrix cores: 4 experts of 2049 x 4097 with 1024 rows 93
+// TFLOP/s (the library's fp32 product 154 at 8192^3); a call of few tiles by
+// the 0.45 us of matrix work that a tile has in each 32-deep slab.
 
 // A tile of the result, one value at a time: rounded once, from the fp32 sum.
 // Old values are loaded all before the first store: a load behind a store
@@ -226,6 +230,19 @@ __device__ __forceinline__ void rows_product(const ExpertCall& c, const RowsTile
 
 // Forward and input gradient on 256 x 256 tiles of eight waves, or the shorter
 // kind that holds the tile's rows.
+//
+// 32768 rows over 61 of 64 experts, 2048 x 7168: 1.00-1.07 ms, 0.90-0.96
+// PFLOP/s of products that count (13% more are computed for rows that pad a
+// tile); 64 experts with 512 rows each 0.90 ms, 1.07 PFLOP/s; one expert of
+// 8192^2 with 8192 rows 1.28 PFLOP/s, where the library's dense product takes
+// 1.38.  Counters: matrix cores busy for 58% of the cycles, LDS bank conflicts
+// 1%, 2.7 GB fetched for 2.3 GB of operands.  What bounds it is the copy path
+// into LDS: each expert's weights are used by two or three row tiles only, so a
+// third of the slabs come from beyond the L2 (a fifth in a dense product).
+// Slabs of 32 in four or five stages: 9% slower, and no difference between the
+// two: more slabs in flight do not help, half-line copies cost.  Three stages for
+// tiles of at most 128 rows: 8% slower where they run beside tall ones, which
+// they outrun, so that the weights are fetched twice.
 template <ExpertOp OP, int CAP>
 __global__ __launch_bounds__(512) void expert_rows_kernel(ExpertCall c, ExpertPtrs<CAP> w, int ntiles) {
     constexpr int S = kBN * 64;
@@ -264,7 +281,9 @@ __global__ __launch_bounds__(256) void expert_mid_kernel(ExpertCall c, ExpertPtr
 
 // Few rows a group: reading the weights is what it takes.  32 x 64 tiles of
 // two waves, four stages, three workgroups a compute unit: three slabs of 8 KB
-// of weights in flight each, and enough tiles to go round.
+// of weights in flight each, and enough tiles to go round.  HBM bounds it: 64
+// rows over 41 of 64 experts (1.2 GB of weights) 202-206 us, 5.9 TB/s, where the
+// 256 x 256 tiles took 300 (328 of them for 256 compute units).
 constexpr int kFewM = 32, kFewN = 64;
 // Mean rows of a group up to which it is taken.  64 experts of 2048 x 7168,
 // against the 256 x 256 tiles: forward at 32 rows 334 and 347 us (at 1 row 311
@@ -487,8 +506,10 @@ hipError_t launch_bf16(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& 
 
 // ---- bf16 of any alignment and size -------------------------------------------
 
-// T x T tiles of four waves through registers; blocks as in the kernels for
-// any type.
+// T x T tiles of four waves through registers; blocks as in the fp32 kernels.
+// Bound by the registers' way into LDS and by value-aligned accesses: 8 experts
+// of 1001 x 2057, 512 rows each, forward 53 us (317 TFLOP/s; 34 us at 1000 x
+// 2056 on the kernels above), 2 experts of 2613 x 3776 with 8 rows 56 us.
 template <ExpertOp OP, int T, int CAP>
 __global__ __launch_bounds__(256) void expert_rows_loose_kernel(ExpertCall c, ExpertPtrs<CAP> w, int ntiles) {
     constexpr bool QKM = OP == kExpertGradInput;
@@ -566,7 +587,8 @@ hipError_t launch_any(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& w
     // at most this many row tiles: every group may end in a ragged one
     const int64_t mt = c.tokens / T + (c.tokens < c.experts ? c.tokens : c.experts);
     if (c.bf16) {
-        // 128 x 128 tiles where they fill the chip twice
+        // 128 x 128 tiles where they fill the chip twice (4 experts of 2049 x
+        // 4097, 1024 rows: 227 us), else 64 x 64
         const int64_t tiles = op == kExpertGradWeight ? c.experts * nr * nc : mt * (op == kExpertForward ? nr : nc);
         return tiles >= 4 * 1024 ? launch_loose<128, CAP>(op, c, w, st) : launch_loose<64, CAP>(op, c, w, st);
     }

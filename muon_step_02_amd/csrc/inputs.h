@@ -21,7 +21,9 @@ constexpr int kGradUnits = 1024;
 // Workgroups of the sum-of-squares launches of one call together, and with
 // them the partial sums the second pass adds up (one more per launch at most).
 constexpr int kGradBlocks = 2048;
-// Lists of at most this many chunks go through one workgroup in one launch.
+// Lists of at most this many chunks (one each for its four teams of 256
+// threads) go through one workgroup in one launch: 5 us, against 3 + 4 us and
+// the gap between two launches.
 constexpr int kGradSingle = 4;
 
 template <int CAP>
