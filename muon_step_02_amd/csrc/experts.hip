@@ -216,11 +216,14 @@ __device__ __forceinline__ bool rows_tile_of(const ExpertCall& c, const ExpertPt
     return true;
 }
 
-template <class C>
-__device__ __forceinline__ void rows_product(const ExpertCall& c, const RowsTile& t, const bf::Stages<C::NS>& st) {
+template <class C, class S>
+__device__ __forceinline__ void rows_product(const ExpertCall& c, const RowsTile& t, const S& st) {
     bf::f32x16 acc[C::FM][C::FN];
     bf::zero<C>(acc);
-    bf::product<C>(acc, t.p, t.q, t.K, st);
+    if constexpr (std::is_same<S, bf::TurnStages>::value)
+        bf::product_in_turns<C>(acc, t.p, t.q, t.K, st);
+    else
+        bf::product<C>(acc, t.p, t.q, t.K, st);
     const int64_t ld = c.ld_c;
     bf::for_each_chunk<C>(acc, reinterpret_cast<float*>(st.q[0]), t.rows, [](int) {},
                           [&](int, int, int r, int c8, const float* v) {
@@ -231,23 +234,19 @@ __device__ __forceinline__ void rows_product(const ExpertCall& c, const RowsTile
 // Forward and input gradient on 256 x 256 tiles of eight waves, or the shorter
 // kind that holds the tile's rows.
 //
-// 32768 rows over 61 of 64 experts, 2048 x 7168: 1.00-1.07 ms, 0.90-0.96
-// PFLOP/s of products that count (13% more are computed for rows that pad a
-// tile); 64 experts with 512 rows each 0.90 ms, 1.07 PFLOP/s; one expert of
-// 8192^2 with 8192 rows 1.28 PFLOP/s, where the library's dense product takes
-// 1.38.  Counters: matrix cores busy for 58% of the cycles, LDS bank conflicts
-// 1%, 2.7 GB fetched for 2.3 GB of operands.  What bounds it is the copy path
-// into LDS: each expert's weights are used by two or three row tiles only, so a
-// third of the slabs come from beyond the L2 (a fifth in a dense product).
-// Slabs of 32 in four or five stages: 9% slower, and no difference between the
-// two: more slabs in flight do not help, half-line copies cost.  Three stages for
-// tiles of at most 128 rows: 8% slower where they run beside tall ones, which
-// they outrun, so that the weights are fetched twice.
+// 32768 rows over 61 of 64 experts, 2048 x 7168: 880 us, 1.09 PFLOP/s of
+// products that count (13% more are computed for rows that pad a tile); 64
+// experts with 512 rows each 780 us, 1.24 PFLOP/s; one expert with all those rows
+// 682 us, 1.41 PFLOP/s, where the library's dense product takes 618.  With both
+// waves of a SIMD reading and multiplying at the same time (product()) the three
+// took 1000, 880 and 786 us.  What bounds it now are the matrix cores' power (the
+// dense product of zeros takes 535 us, the library's 530) and the weights, which
+// two or three row tiles share.
 template <ExpertOp OP, int CAP>
 __global__ __launch_bounds__(512) void expert_rows_kernel(ExpertCall c, ExpertPtrs<CAP> w, int ntiles) {
     constexpr int S = kBN * 64;
-    __shared__ __attribute__((aligned(1024))) uint16_t l0[S], l1[S], l2[S], l3[S];
-    const bf::Stages<2> st{{l0, l2}, {l1, l3}};
+    __shared__ __attribute__((aligned(1024))) uint16_t p0[S], p1[S], q0[S], q1[S], q2[S];
+    const bf::TurnStages st{{p0, p1}, {q0, q1, q2}};
     RowsTile t;
     if (!rows_tile_of<OP, kBM, kBN, 32>(c, w, ntiles, t)) return;
     constexpr bool QKM = OP == kExpertGradInput;

@@ -164,16 +164,25 @@ __device__ __forceinline__ void mfma_frags(f32x16 (&acc)[C::FM][C::FN], const Fr
 }
 
 template <class C>
-__device__ __forceinline__ void copy_stage(const Operand& p, const Operand& q, int64_t k0, int64_t K,
-                                           uint16_t* sp, uint16_t* sq, int wave, int lane) {
+__device__ __forceinline__ void copy_p(const Operand& p, int64_t k0, int64_t K, uint16_t* sp, int wave, int lane) {
     if constexpr (C::PKM)
         copy_kmajor<C::BM, C::NW, C::BK>(p, k0, sp, wave, lane);
     else
         copy_rows<C::BM, C::NW, C::BK>(p, k0, K, sp, wave, lane);
+}
+template <class C>
+__device__ __forceinline__ void copy_q(const Operand& q, int64_t k0, int64_t K, uint16_t* sq, int wave, int lane) {
     if constexpr (C::QKM)
         copy_kmajor<C::BN, C::NW, C::BK>(q, k0, sq, wave, lane);
     else
         copy_rows<C::BN, C::NW, C::BK>(q, k0, K, sq, wave, lane);
+}
+
+template <class C>
+__device__ __forceinline__ void copy_stage(const Operand& p, const Operand& q, int64_t k0, int64_t K,
+                                           uint16_t* sp, uint16_t* sq, int wave, int lane) {
+    copy_p<C>(p, k0, K, sp, wave, lane);
+    copy_q<C>(q, k0, K, sq, wave, lane);
 }
 
 template <int N>
@@ -273,6 +282,74 @@ __device__ __forceinline__ void product(f32x16 (&acc)[C::FM][C::FN], const Opera
             }
         });
     }
+    wait_vmcnt<0>();
+}
+
+// As product(), for eight waves, two on each SIMD, of which the waves of the
+// tile's lower half run one phase behind those of its upper half: on every
+// SIMD one wave has the matrix cores to itself while the other reads its
+// operands.  A slab is four phases, each ended by a barrier: the fragments of
+// two k-steps are read and copies issued, then multiplied, twice.
+//
+// The two halves read a stage in phases 4 kt ... 4 kt + 3 (slab kt, the lower half
+// from 4 kt + 1), so a stage is free from phase 4 kt + 4 on.  P (rows) has two
+// stages: slab kt + 1 is copied from the first phase of slab kt on.  Q (the
+// weights, which come from farther away) has three: slab kt + 2 is copied from
+// the third phase of slab kt on, and stays in flight at the wait there, which
+// is for slab kt + 1 (the upper half reads it two phases later, behind the
+// barrier that ends this phase of the lower half).
+struct TurnStages {
+    uint16_t *p[2], *q[3];
+};
+template <class C>
+__device__ __forceinline__ void product_in_turns(f32x16 (&acc)[C::FM][C::FN], const Operand& p, const Operand& q,
+                                                 int64_t K, const TurnStages& st) {
+    static_assert(C::NW == 8 && C::WM == 2 && C::BK == 64, "two waves a SIMD, slabs of two times two k-steps");
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const int KT = (int)((K + C::BK - 1) / C::BK);
+    if (KT == 0) return;
+    constexpr int LQ = C::BN * C::BK / 512 / C::NW;  // copies of a wave and slab of Q
+    copy_q<C>(q, 0, K, st.q[0], wave, lane);
+    copy_p<C>(p, 0, K, st.p[0], wave, lane);
+    copy_q<C>(q, C::BK, K, st.q[1], wave, lane);
+    wait_vmcnt<LQ>();
+    lds_barrier();
+    if (wm == 1) __builtin_amdgcn_s_barrier();
+    Frags<C> f[2];
+    auto multiply = [&]() {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+        mfma_frags<C>(acc, f[0]);
+        mfma_frags<C>(acc, f[1]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    auto slab = [&](auto u, int kt) {
+        constexpr int up = u % 2, uq = u % 3;
+        read_frags<C>(st.p[up], st.q[uq], 0, wm, wn, lane, f[0]);
+        read_frags<C>(st.p[up], st.q[uq], 1, wm, wn, lane, f[1]);
+        copy_p<C>(p, (int64_t)(kt + 1) * C::BK, K, st.p[1 - up], wave, lane);
+        lds_barrier();
+        multiply();
+        read_frags<C>(st.p[up], st.q[uq], 2, wm, wn, lane, f[0]);
+        read_frags<C>(st.p[up], st.q[uq], 3, wm, wn, lane, f[1]);
+        copy_q<C>(q, (int64_t)(kt + 2) * C::BK, K, st.q[(u + 2) % 3], wave, lane);
+        wait_vmcnt<LQ>();
+        lds_barrier();
+        multiply();
+    };
+    // whole turns over the stages with no way out between: where one joins the
+    // loop's end the compiler takes the copies of both paths to be in flight
+    int kt = 0;
+    for (; kt + 6 <= KT; kt += 6)
+        unrolled<6>([&](auto u) { slab(u, kt + u); });
+    unrolled<5>([&](auto u) {
+        if (kt + u < KT) slab(u, kt + u);
+    });
+    if (wm == 0) __builtin_amdgcn_s_barrier();
     wait_vmcnt<0>();
 }
 
