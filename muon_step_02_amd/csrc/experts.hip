@@ -221,7 +221,7 @@ __device__ __forceinline__ void rows_product(const ExpertCall& c, const RowsTile
     bf::f32x16 acc[C::FM][C::FN];
     bf::zero<C>(acc);
     if constexpr (std::is_same<S, bf::TurnStages>::value)
-        bf::product_in_turns<C>(acc, t.p, t.q, t.K, st);
+        bf::product_in_turns<C>(acc, t.p, t.q, t.K, t.rows, st);
     else
         bf::product<C>(acc, t.p, t.q, t.K, st);
     const int64_t ld = c.ld_c;

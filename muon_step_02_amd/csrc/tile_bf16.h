@@ -154,13 +154,18 @@ __device__ __forceinline__ void read_frags(const uint16_t* sp, const uint16_t* s
                         : frag_rows<C::BK>(sq, wn * C::TN + j * 32 + row, chunk);
 }
 
-template <class C>
-__device__ __forceinline__ void mfma_frags(f32x16 (&acc)[C::FM][C::FN], const Frags<C>& f) {
+// Blocks of rows [I0, I1).
+template <class C, int I0, int I1>
+__device__ __forceinline__ void mfma_rows(f32x16 (&acc)[C::FM][C::FN], const Frags<C>& f) {
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i)
+    for (int i = I0; i < I1; ++i)
 #pragma unroll
         for (int j = 0; j < C::FN; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[i], f.b[j], acc[i][j], 0, 0, 0);
+}
+template <class C>
+__device__ __forceinline__ void mfma_frags(f32x16 (&acc)[C::FM][C::FN], const Frags<C>& f) {
+    mfma_rows<C, 0, C::FM>(acc, f);
 }
 
 template <class C>
@@ -285,6 +290,10 @@ __device__ __forceinline__ void product(f32x16 (&acc)[C::FM][C::FN], const Opera
     wait_vmcnt<0>();
 }
 
+struct TurnStages {
+    uint16_t *p[2], *q[3];
+};
+
 // As product(), for eight waves, two on each SIMD, of which the waves of the
 // tile's lower half run one phase behind those of its upper half: on every
 // SIMD one wave has the matrix cores to itself while the other reads its
@@ -298,12 +307,12 @@ __device__ __forceinline__ void product(f32x16 (&acc)[C::FM][C::FN], const Opera
 // the third phase of slab kt on, and stays in flight at the wait there, which
 // is for slab kt + 1 (the upper half reads it two phases later, behind the
 // barrier that ends this phase of the lower half).
-struct TurnStages {
-    uint16_t *p[2], *q[3];
-};
+//
+// rows: the tile's valid rows.  Where they end 32 rows or more before the tile
+// does, the lower half leaves its last row of blocks out.
 template <class C>
 __device__ __forceinline__ void product_in_turns(f32x16 (&acc)[C::FM][C::FN], const Operand& p, const Operand& q,
-                                                 int64_t K, const TurnStages& st) {
+                                                 int64_t K, int rows, const TurnStages& st) {
     static_assert(C::NW == 8 && C::WM == 2 && C::BK == 64, "two waves a SIMD, slabs of two times two k-steps");
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / C::WN, wn = wave % C::WN;
@@ -316,12 +325,16 @@ __device__ __forceinline__ void product_in_turns(f32x16 (&acc)[C::FM][C::FN], co
     wait_vmcnt<LQ>();
     lds_barrier();
     if (wm == 1) __builtin_amdgcn_s_barrier();
+    const bool whole = wm == 0 || rows > C::BM - 32;
     Frags<C> f[2];
     auto multiply = [&]() {
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_setprio(1);
-        mfma_frags<C>(acc, f[0]);
-        mfma_frags<C>(acc, f[1]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) mfma_rows<C, 0, C::FM - 1>(acc, f[h]);
+        if (whole)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) mfma_rows<C, C::FM - 1, C::FM>(acc, f[h]);
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
