@@ -440,13 +440,15 @@ bool chunked(ExpertOp op, const ExpertCall& c, const void* const* w) {
     return true;
 }
 
-// Which tile is faster, by the rounds each takes on 256 compute units.
-// Measured per 64-deep slab and round: 1.33 us for 256 x 256 tiles, 1.15 us for
-// 128 x 128 tiles at two a compute unit, 0.76 us at one.  (8 experts of 1024 x
-// 1024, 512 rows each: 28.4 and 15.5 us; 8 of 2056 outputs, 512 rows, K = 1000,
-// 144 and 544 tiles: 33.8 and 41.6 us.)
+// Whether 128 x 128 tiles take less time than 256 x 256 ones: in hundredths of
+// a microsecond a slab, a round of 256 big tiles takes 110, and 8 in all go to
+// the longer start; a round of 512 small ones, two a compute unit, 115, of up
+// to 256 76.  Measured, big and small: 8 experts of 1024 x 1024, 512 rows each
+// (64 and 256 tiles) 26.0 and 16.0 us; 16 of 2048 x 2048, 256 rows (128 and
+// 512) 41.9 and 41.4; 64 of 2048 x 7168, 128 rows (512 and 1024) 359 and 390; 8
+// of 2056 outputs, 512 rows, K = 1000 (144 and 544) 29.0 and 40.9.
 bool mid_tiles(int64_t big, int64_t mid) {
-    const int64_t tb = (big + 255) / 256 * 133;
+    const int64_t tb = (big + 255) / 256 * 110 + 8;
     const int64_t rest = mid % 512;
     const int64_t tm = mid / 512 * 115 + (rest == 0 ? 0 : rest <= 256 ? 76 : 115);
     return tm < tb;

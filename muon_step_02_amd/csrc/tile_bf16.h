@@ -329,13 +329,11 @@ __device__ __forceinline__ void product_in_turns(f32x16 (&acc)[C::FM][C::FN], co
     Frags<C> f[2];
     auto multiply = [&]() {
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int h = 0; h < 2; ++h) mfma_rows<C, 0, C::FM - 1>(acc, f[h]);
         if (whole)
 #pragma unroll
             for (int h = 0; h < 2; ++h) mfma_rows<C, C::FM - 1, C::FM>(acc, f[h]);
-        __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
