@@ -321,8 +321,8 @@ struct TurnStages {
 // stages: slab kt + 1 is copied from the first phase of slab kt on.  Q (the
 // weights, which come from farther away) has three: slab kt + 2 is copied from
 // the third phase of slab kt on, and stays in flight at the wait there, which
-// is for slab kt + 1 (the upper half reads it two phases later, behind the
-// barrier that ends this phase of the lower half).
+// is for slab kt + 1: the upper half waits in phase 4 kt + 2, the lower one in 4 kt
+// + 3, and the first read is in 4 kt + 4.
 //
 // rows: the tile's valid rows.  Where they end 32 rows or more before the tile
 // does, the lower half leaves its last row of blocks out.
@@ -340,7 +340,14 @@ __device__ __forceinline__ void product_in_turns(f32x16 (&acc)[C::FM][C::FN], co
     copy_q<C>(q, C::BK, K, st.q[1], wave, lane);
     wait_vmcnt<LQ>();
     lds_barrier();
-    if (wm == 1) __builtin_amdgcn_s_barrier();
+    // a barrier that no LDS read or copy is moved over
+    auto meet = []() {
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_s_barrier();
+        __atomic_signal_fence(__ATOMIC_SEQ_CST);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    if (wm == 1) meet();
     const bool whole = wm == 0 || rows > C::BM - 32;
     Frags<C> f[2];
     auto multiply = [&]() {
@@ -351,8 +358,7 @@ __device__ __forceinline__ void product_in_turns(f32x16 (&acc)[C::FM][C::FN], co
 #pragma unroll
             for (int h = 0; h < 2; ++h) mfma_rows<C, C::FM - 1, C::FM>(acc, f[h]);
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
+        meet();
     };
     auto slab = [&](auto u, int kt) {
         constexpr int up = u % 2, uq = u % 3;
@@ -376,7 +382,7 @@ __device__ __forceinline__ void product_in_turns(f32x16 (&acc)[C::FM][C::FN], co
     unrolled<5>([&](auto u) {
         if (kt + u < KT) slab(u, kt + u);
     });
-    if (wm == 0) __builtin_amdgcn_s_barrier();
+    if (wm == 0) meet();
     wait_vmcnt<0>();
 }
 
