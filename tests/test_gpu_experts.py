@@ -347,3 +347,14 @@ def test_binding_refuses():
     with pytest.raises(mu.MuonError) as e:
         mu.muon_expert_grad_input(h, ex, L.offsets, L.dy, L.w[0].as_strided(L.dx.shape, (24, 1), 0))
     assert e.value.status == 4
+
+
+# Groups whose tiles end in each of the eight 32-row blocks of a 256-row tile,
+# wide enough that 256-wide tiles are taken (forward, and the input gradient with
+# the widths exchanged); K of one to thirteen slabs, whole and ragged, so that
+# the loop over six slabs ends at each of them.
+@pytest.mark.parametrize("k", [8, 64, 72, 128, 192, 264, 320, 384, 392, 456, 512, 640, 704, 768, 776])
+def test_wide_tiles(k):
+    sizes = [225, 193, 200, 161, 100, 33, 256, 1, 289]
+    Layer(sizes, 4104, k, BF16, seed=k).check()
+    Layer(sizes, k, 4104, BF16, seed=k + 1, pad=8).check()
