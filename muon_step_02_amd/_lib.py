@@ -132,6 +132,7 @@ class MuonGrad(ctypes.Structure):
         ("grad_dtype", ctypes.c_int32),
         ("out_dtype", ctypes.c_int32),
     ]
+    _device = None  # of the tensors it was made of (muon_grad)
 
 
 class MuonExperts(ctypes.Structure):
@@ -492,6 +493,8 @@ def _rows_of(t):
 def muon_grad(grad, out=None):
     """Descriptor of one gradient for :func:`muon_grad_norm` and, with ``out``
     (the gradient itself clips in place), :func:`muon_grad_clip`."""
+    if out is not None and out.device != grad.device:
+        raise ValueError("the gradient is on %s, its output on %s" % (grad.device, out.device))
     rows, cols, ld = _rows_of(grad)
     g = MuonGrad(grad=grad.data_ptr(), rows=rows, cols=cols, ld_grad=ld, grad_dtype=_dt(grad))
     if out is not None:
@@ -504,6 +507,7 @@ def muon_grad(grad, out=None):
                 raise ValueError("grad and out layouts differ")
             g.rows, g.cols, g.ld_grad, old = 1, grad.numel(), grad.numel(), grad.numel()
         g.out, g.ld_out, g.out_dtype = out.data_ptr(), old, _dt(out)
+    g._device = grad.device
     return g
 
 
@@ -516,8 +520,13 @@ def muon_grad_workspace_size(h, grads):
 
 
 def _grad_call(name, h, grads, max_norm, workspace, norm_out, scale_out, stream):
-    arr = grads if isinstance(grads, ctypes.Array) else (MuonGrad * len(grads))(*grads)
     dev = _same_device(workspace, norm_out, scale_out)
+    arr = grads
+    if not isinstance(grads, ctypes.Array):  # (whose structures have lost their tensors)
+        for g in grads:
+            if g._device is not None and g._device != dev:
+                raise ValueError("a gradient is on %s, the workspace on %s" % (g._device, dev))
+        arr = (MuonGrad * len(grads))(*grads)
     _check(getattr(load(), name)(h, arr, len(arr), float(max_norm), _scalar(norm_out, "norm_out"),
                                  _scalar(scale_out, "scale_out"), workspace.data_ptr(),
                                  _nbytes(workspace), _stream_on(stream, dev, h)), name)

@@ -291,3 +291,53 @@ def test_smax_workspace_holds_every_partial(lib, handle):
         qk = _qk(tokens_q=tq, sequences=seqs, heads_q=heads, heads_k=1)
         assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(qk), ctypes.byref(sz)) == 0
         assert sz.value % 256 == 0 and sz.value >= 4 * heads * (tq // 256)
+
+
+# ---- the binding without a GPU ------------------------------------------------
+
+class _On:
+    """Stands in for a tensor on a device that this machine need not have."""
+
+    def __init__(self, device, *shape, dtype=torch.float32, stride=None):
+        self._t = torch.zeros(shape, dtype=dtype)
+        if stride is not None:
+            self._t = self._t.as_strided(shape, stride)
+        self.device = torch.device(device)
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+class _NoCalls:
+    """Stands in for the library: any entry point that is reached fails."""
+
+    def __getattr__(self, name):
+        raise AssertionError("%s was called" % name)
+
+
+@pytest.fixture
+def bound(monkeypatch):
+    """A handle of device 0, with a library that nothing may call."""
+    from muon_step_02_amd import _lib
+    monkeypatch.setattr(_lib, "load", _NoCalls)
+    h = ctypes.c_void_p(BUF)
+    h.device = 0
+    return h
+
+
+@pytest.mark.parametrize("device", ["cpu", "cuda:1"])
+@pytest.mark.parametrize("call", [mu.muon_grad_norm, mu.muon_grad_clip])
+def test_gradients_of_another_device_are_refused(bound, call, device):
+    ws, norm = _On("cuda:0", 64, dtype=torch.uint8), _On("cuda:0", 1)
+    here, there = _On("cuda:0", 4, 8), _On(device, 4, 8)
+    for plan in ([mu.muon_grad(there, there)], [mu.muon_grad(here, here), mu.muon_grad(there, there)]):
+        with pytest.raises(ValueError):
+            call(bound, plan, 1.0, ws, norm_out=norm, stream=0)
+    with pytest.raises(AssertionError):  # the same call with every tensor in place gets through
+        call(bound, [mu.muon_grad(here, here)], 1.0, ws, norm_out=norm, stream=0)
+
+
+def test_an_output_on_another_device_than_its_gradient_is_refused():
+    for device in ("cpu", "cuda:1"):
+        with pytest.raises(ValueError):
+            mu.muon_grad(_On("cuda:0", 8), _On(device, 8))
