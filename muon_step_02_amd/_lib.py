@@ -508,6 +508,7 @@ def muon_grad(grad, out=None):
             g.rows, g.cols, g.ld_grad, old = 1, grad.numel(), grad.numel(), grad.numel()
         g.out, g.ld_out, g.out_dtype = out.data_ptr(), old, _dt(out)
     g._device = grad.device
+    g._keepalive = (grad, out)
     return g
 
 

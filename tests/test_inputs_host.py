@@ -341,3 +341,17 @@ def test_an_output_on_another_device_than_its_gradient_is_refused():
     for device in ("cpu", "cuda:1"):
         with pytest.raises(ValueError):
             mu.muon_grad(_On("cuda:0", 8), _On(device, 8))
+
+
+def test_gradient_descriptors_keep_their_tensors():
+    import gc
+    import weakref
+    g, o = torch.zeros(4, 8), torch.zeros(4, 8)
+    alive = [weakref.ref(t) for t in (g, o)]
+    plan = [mu.muon_grad(g, o)]
+    del g, o
+    gc.collect()
+    assert all(r() is not None for r in alive)
+    del plan
+    gc.collect()
+    assert all(r() is None for r in alive)
