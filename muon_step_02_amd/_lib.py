@@ -555,6 +555,8 @@ def muon_experts(weights):
     for w in weights:
         if w.shape != w0.shape or w.dtype != w0.dtype or (w.shape[0] > 1 and _ld(w) != ld):
             raise ValueError("the experts' shapes, types or leading dimensions differ")
+        if w.shape[1] > 1 and w.stride(1) != 1:
+            raise ValueError("expected 2D row-major tensors (stride(1) == 1)")
     ptrs = (ctypes.c_void_p * len(weights))(*[w.data_ptr() for w in weights])
     ex = MuonExperts(weights=ptrs, rows=w0.shape[0], cols=w0.shape[1], ld=ld, experts=len(weights),
                      dtype=_dt(w0))

@@ -355,3 +355,18 @@ def test_gradient_descriptors_keep_their_tensors():
     del plan
     gc.collect()
     assert all(r() is None for r in alive)
+
+
+def test_one_row_experts_with_a_column_stride_are_refused():
+    """One row has no leading dimension, but its columns still have to follow
+    each other."""
+    apart = _On("cuda:0", 1, 8, stride=(16, 2))
+    with pytest.raises(ValueError):
+        mu.muon_experts([apart])
+    with pytest.raises(ValueError):
+        mu.muon_experts([_On("cuda:0", 1, 8), apart])
+    ex = mu.muon_experts([_On("cuda:0", 1, 8), _On("cuda:0", 1, 8, stride=(16, 1))])
+    assert (ex.rows, ex.cols, ex.ld) == (1, 8, 8)
+    # a column of one value a row
+    ex = mu.muon_experts([_On("cuda:0", 1, 1, stride=(1, 5))])
+    assert (ex.rows, ex.cols, ex.ld) == (1, 1, 1)
