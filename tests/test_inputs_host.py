@@ -301,7 +301,7 @@ class _On:
     def __init__(self, device, *shape, dtype=torch.float32, stride=None):
         self._t = torch.zeros(shape, dtype=dtype)
         if stride is not None:
-            self._t = self._t.as_strided(shape, stride)
+            self._t = torch.zeros(1024, dtype=dtype).as_strided(shape, stride)
         self.device = torch.device(device)
 
     def __getattr__(self, name):
