@@ -434,6 +434,8 @@ def _stream_on(stream, device, h):
     if stream is None:
         import torch
         return torch.cuda.current_stream(device.index).cuda_stream
+    if getattr(stream, "device", device) != device:
+        raise ValueError("the tensors are on %s, the stream on %s" % (device, stream.device))
     return _stream_ptr(stream)
 
 

@@ -312,7 +312,9 @@ class _NoCalls:
     """Stands in for the library: any entry point that is reached fails."""
 
     def __getattr__(self, name):
-        raise AssertionError("%s was called" % name)
+        def called(*args):
+            raise AssertionError("%s was called" % name)
+        return called
 
 
 @pytest.fixture
@@ -370,3 +372,17 @@ def test_one_row_experts_with_a_column_stride_are_refused():
     # a column of one value a row
     ex = mu.muon_experts([_On("cuda:0", 1, 1, stride=(1, 5))])
     assert (ex.rows, ex.cols, ex.ld) == (1, 1, 1)
+
+
+def test_a_stream_of_another_device_is_refused(bound):
+    class Stream:
+        cuda_stream = 0
+
+        def __init__(self, device):
+            self.device = torch.device(device)
+
+    ws, norm, g = _On("cuda:0", 64, dtype=torch.uint8), _On("cuda:0", 1), _On("cuda:0", 8)
+    with pytest.raises(ValueError):
+        mu.muon_grad_norm(bound, [mu.muon_grad(g)], 1.0, ws, norm_out=norm, stream=Stream("cuda:1"))
+    with pytest.raises(AssertionError):  # gets through
+        mu.muon_grad_norm(bound, [mu.muon_grad(g)], 1.0, ws, norm_out=norm, stream=Stream("cuda:0"))
