@@ -309,7 +309,8 @@ muon_status muon_grad_workspace_size(muon_handle h, const muon_grad* gs, int n, 
  * workspace: muon_grad_workspace_size bytes, 256-byte aligned, not shared by
  * calls that may overlap in time.  Rejects n < 1, negative sizes, ld < cols,
  * a null grad, unknown dtypes, max_norm <= 0 or non-finite, a small or null
- * workspace. */
+ * workspace, and a workspace, norm_out or scale_out that shares memory with
+ * another of them or with a tensor (MUON_ERR_OVERLAP). */
 muon_status muon_grad_norm(muon_handle h, const muon_grad* gs, int n, float max_norm,
                            float* norm_out, float* scale_out, void* workspace,
                            size_t workspace_bytes, void* stream);

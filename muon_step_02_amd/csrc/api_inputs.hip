@@ -27,7 +27,8 @@ Rect rect_of(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es, b
 }
 
 // Whether two ranges share bytes.  Column blocks of one buffer (the same row
-// stride, disjoint columns) interleave without sharing any.
+// stride, disjoint columns) interleave without sharing any, and so does what
+// lies between a tensor's rows.
 bool collide(const Rect& a, const Rect& b) {
     if (a.hi <= b.lo || b.hi <= a.lo) return false;
     if (a.stride == b.stride) {
@@ -36,7 +37,19 @@ bool collide(const Rect& a, const Rect& b) {
         const size_t d = (s.lo - f.lo) % f.stride;
         return d < f.width || d + s.width > f.stride;
     }
-    return true;
+    if (a.width != a.stride && b.width != b.stride) return true;
+    // one of them is one run of bytes: against the other's rows
+    const Rect& run = a.width == a.stride ? a : b;
+    const Rect& r = a.width == a.stride ? b : a;
+    if (run.lo <= r.lo) return true;
+    const size_t d = (run.lo - r.lo) % r.stride;
+    const uintptr_t next = run.lo + (r.stride - d);  // the row behind run.lo
+    return d < r.width || (next < run.hi && next < r.hi);
+}
+
+Rect run_of(const void* p, size_t bytes, bool write, int owner) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+    return Rect{b, b + bytes, bytes, bytes, write, owner};
 }
 
 // Whether a written range shares bytes with any other range, one owner's
@@ -128,6 +141,29 @@ size_t grad_workspace_bytes(int n) {
     return align_up(parts * sizeof(double), 256);
 }
 
+// The workspace and the scalars, all of them written, share no memory with each
+// other or with a tensor: blocks read one while others write the other.
+muon_status check_grad_scalars(const muon_grad* gs, int n, bool clip, const float* norm_out,
+                               const float* scale_out, const void* workspace) {
+    Rect w[3];
+    int k = 0;
+    w[k++] = run_of(workspace, grad_workspace_bytes(n), true, 0);
+    if (norm_out) w[k++] = run_of(norm_out, 4, true, 1);
+    if (scale_out) w[k++] = run_of(scale_out, 4, true, 2);
+    for (int i = 1; i < k; ++i)
+        for (int j = 0; j < i; ++j)
+            if (collide(w[i], w[j])) return MUON_ERR_OVERLAP;
+    for (int t = 0; t < n; ++t) {
+        const muon_grad& g = gs[t];
+        if (g.rows == 0 || g.cols == 0) continue;
+        const Rect a = rect_of(g.grad, g.rows, g.cols, g.ld_grad, elem_bytes(g.grad_dtype), false, 0);
+        const Rect b = clip ? rect_of(g.out, g.rows, g.cols, g.ld_out, elem_bytes(g.out_dtype), true, 0) : a;
+        for (int i = 0; i < k; ++i)
+            if (collide(w[i], a) || collide(w[i], b)) return MUON_ERR_OVERLAP;
+    }
+    return MUON_OK;
+}
+
 // Calls fn(group, chunks of the group) for the tensors of each launch.
 template <int CAP, class F>
 hipError_t for_each_grad_group(const muon_grad* gs, int n, bool clip, F&& fn) {
@@ -213,6 +249,8 @@ muon_status grad_call(muon_handle h, const muon_grad* gs, int n, bool clip, floa
     }
     if (!workspace || misaligned(workspace, 256) || workspace_bytes < grad_workspace_bytes(n))
         return MUON_ERR_WORKSPACE;
+    st = check_grad_scalars(gs, n, clip, norm_out, scale_out, workspace);
+    if (st != MUON_OK) return st;
     DeviceGuard g(h->device);
     double* partials = reinterpret_cast<double*>(workspace);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);

@@ -233,3 +233,18 @@ def test_binding_refuses():
     with pytest.raises(mu.MuonError) as e:
         mu.muon_grad_norm(h, plan, 1.0, ws[:128], norm_out=torch.zeros(1, device=DEV))
     assert e.value.status == 3
+
+
+def test_scalars_between_the_rows_of_a_gradient():
+    """Padding belongs to no tensor: norm and scale may lie in it."""
+    h = Handle.get()
+    buf = torch.randn(300, 136, device=DEV)
+    g = buf[:, :128]
+    before = g.clone()
+    norm, scale = _reference([before], 2.0)
+    assert norm > 2.0
+    plan = [mu.muon_grad(g, g)]
+    mu.muon_grad_clip(h, plan, 2.0, _workspace(h, plan), norm_out=buf[0, 128:129], scale_out=buf[7, 135:136])
+    _check_norm(buf[0, 128], norm)
+    assert abs(float(buf[7, 135]) - scale) <= NORM_TOL * scale
+    _check_outs([before], [g], scale)

@@ -386,3 +386,34 @@ def test_a_stream_of_another_device_is_refused(bound):
         mu.muon_grad_norm(bound, [mu.muon_grad(g)], 1.0, ws, norm_out=norm, stream=Stream("cuda:1"))
     with pytest.raises(AssertionError):  # gets through
         mu.muon_grad_norm(bound, [mu.muon_grad(g)], 1.0, ws, norm_out=norm, stream=Stream("cuda:0"))
+
+
+# ---- ranges that a call writes ------------------------------------------------
+
+@pytest.mark.parametrize("clip", [False, True])
+def test_grad_scalars_that_share_memory_are_refused(lib, handle, clip):
+    ws = 8 * BUF
+    need = ctypes.c_size_t()
+    g = _grad(out=2 * BUF)          # 128 bytes at BUF and at 2 BUF
+    assert lib.muon_grad_workspace_size(handle, ctypes.byref(g), 1, ctypes.byref(need)) == 0
+
+    def call(**kw):
+        return _grad_call(lib, handle, [_grad(grad=3 * BUF, out=3 * BUF), g], clip, **kw)
+
+    far = 6 * BUF
+    for at in (ws, ws + 256, ws + need.value - 4, BUF, BUF + 64, BUF + 124):
+        assert call(norm=at) == OVERLAP
+        assert call(norm=far, scale=at) == OVERLAP
+    assert call(norm=far, scale=far) == OVERLAP         # on each other
+    if clip:
+        for at in (2 * BUF, 2 * BUF + 124, 3 * BUF):
+            assert call(norm=at) == OVERLAP
+            assert call(norm=far, scale=at) == OVERLAP
+
+
+@pytest.mark.parametrize("clip", [False, True])
+def test_gradients_in_the_workspace_are_refused(lib, handle, clip):
+    for at in (8 * BUF, 8 * BUF + 1024, 8 * BUF - 64):
+        assert _grad_call(lib, handle, [_grad(out=3 * BUF), _grad(grad=at, out=2 * BUF)], clip, norm=6 * BUF) == OVERLAP
+    if clip:
+        assert _grad_call(lib, handle, [_grad(out=8 * BUF + 64)], norm=6 * BUF) == OVERLAP
