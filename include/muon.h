@@ -397,7 +397,9 @@ typedef struct {
  * of its unmasked logits is; masked pairs never count.  accumulate: the larger
  * of the result and what the output holds (micro-batches).
  * workspace: as above, muon_qk_smax_workspace_size bytes (it depends on the
- * sizes, not on pointers). */
+ * sizes, not on pointers).  Rejects sizes and strides out of range, null or
+ * misaligned pointers, a small or null workspace, and outputs or a workspace
+ * that share memory with anything else of the call (MUON_ERR_OVERLAP). */
 muon_status muon_qk_smax_workspace_size(muon_handle h, const muon_qk* qk, size_t* bytes);
 muon_status muon_qk_smax(muon_handle h, const muon_qk* qk, float* smax_q, float* smax_k,
                          int accumulate, void* workspace, size_t workspace_bytes, void* stream);

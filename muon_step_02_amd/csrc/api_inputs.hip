@@ -416,6 +416,11 @@ muon_status muon_expert_grad_weight(muon_handle h, const muon_experts* grads, co
 
 namespace {
 
+// Elements from the first to the last of (tokens, heads, head_dim) values.
+__int128 span(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
+    return tokens > 0 ? (__int128)(tokens - 1) * token + (__int128)(heads - 1) * head + dim : 0;
+}
+
 // parts: the most partial maxima either kernel's plan has for these sizes.
 muon_status check_qk(const muon_qk* s, SmaxCall* c, int64_t* parts, muon_handle h) {
     if (!s) return MUON_ERR_INVALID_ARG;
@@ -429,6 +434,9 @@ muon_status check_qk(const muon_qk* s, SmaxCall* c, int64_t* parts, muon_handle 
     constexpr int64_t lim = (int64_t)1 << 40;
     if (s->q_token < 0 || s->q_head < 0 || s->k_token < 0 || s->k_head < 0 || s->q_token > lim ||
         s->q_head > lim || s->k_token > lim || s->k_head > lim)
+        return MUON_ERR_INVALID_ARG;
+    if (span(s->tokens_q, s->q_token, s->heads_q, s->q_head, s->head_dim) > lim ||
+        span(s->tokens_k, s->k_token, s->heads_k, s->k_head, s->head_dim) > lim)
         return MUON_ERR_INVALID_ARG;
     c->q = s->q;
     c->k = s->k;
@@ -453,6 +461,28 @@ muon_status check_qk(const muon_qk* s, SmaxCall* c, int64_t* parts, muon_handle 
     return *parts > INT32_MAX ? MUON_ERR_INVALID_ARG : MUON_OK;
 }
 
+// Outputs and workspace share no memory with anything else of the call: blocks
+// write them while others read the rest.
+muon_status check_qk_overlap(const muon_qk* s, const float* smax_q, const float* smax_k, const void* workspace,
+                             size_t workspace_bytes) {
+    const size_t es = elem_bytes(s->dtype), cu = (size_t)(s->sequences + 1) * 4;
+    const size_t q = (size_t)span(s->tokens_q, s->q_token, s->heads_q, s->q_head, s->head_dim) * es;
+    const size_t k = (size_t)span(s->tokens_k, s->k_token, s->heads_k, s->k_head, s->head_dim) * es;
+    Rect r[7];
+    int n = 0;
+    auto add = [&](const void* p, size_t bytes, bool write) {
+        if (bytes) r[n] = run_of(p, bytes, write, n), ++n;
+    };
+    add(s->q, q, false);
+    add(s->k, k, false);
+    add(s->cu_q, cu, false);
+    add(s->cu_k, cu, false);
+    add(workspace, workspace_bytes, true);
+    add(smax_q, smax_q ? (size_t)s->heads_q * 4 : 0, true);
+    add(smax_k, smax_k ? (size_t)s->heads_k * 4 : 0, true);
+    return any_collision(r, n) ? MUON_ERR_OVERLAP : MUON_OK;
+}
+
 size_t smax_workspace_bytes(int64_t parts) { return align_up((size_t)parts * sizeof(float) + 256, 256); }
 
 }  // namespace
@@ -474,7 +504,7 @@ muon_status muon_qk_smax(muon_handle h, const muon_qk* qk, float* smax_q, float*
     if (!h) return MUON_ERR_INVALID_ARG;
     SmaxCall c{};
     int64_t parts = 0;
-    const muon_status st = check_qk(qk, &c, &parts, h);
+    muon_status st = check_qk(qk, &c, &parts, h);
     if (st != MUON_OK) return st;
     if (!smax_q && !smax_k) return MUON_ERR_INVALID_ARG;
     if (accumulate != 0 && accumulate != 1) return MUON_ERR_INVALID_ARG;
@@ -485,6 +515,8 @@ muon_status muon_qk_smax(muon_handle h, const muon_qk* qk, float* smax_q, float*
         return MUON_ERR_UNALIGNED;
     if (!workspace || misaligned(workspace, 256) || workspace_bytes < smax_workspace_bytes(parts))
         return MUON_ERR_WORKSPACE;
+    st = check_qk_overlap(qk, smax_q, smax_k, workspace, smax_workspace_bytes(parts));
+    if (st != MUON_OK) return st;
     DeviceGuard g(h->device);
     return hip_status(launch_smax(c, reinterpret_cast<float*>(workspace), smax_q, smax_k, accumulate,
                                   reinterpret_cast<hipStream_t>(stream)));

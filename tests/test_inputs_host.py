@@ -417,3 +417,28 @@ def test_gradients_in_the_workspace_are_refused(lib, handle, clip):
         assert _grad_call(lib, handle, [_grad(out=3 * BUF), _grad(grad=at, out=2 * BUF)], clip, norm=6 * BUF) == OVERLAP
     if clip:
         assert _grad_call(lib, handle, [_grad(out=8 * BUF + 64)], norm=6 * BUF) == OVERLAP
+
+
+@pytest.mark.parametrize("tokens_q,dtype", [(10, 1), (3000, 0)])
+def test_smax_outputs_and_workspace_that_share_memory_are_refused(lib, handle, tokens_q, dtype):
+    far = dict(q=40 * BUF, k=50 * BUF, ws=60 * BUF)
+    qk = _qk(q=10 * BUF, k=20 * BUF, cu_q=30 * BUF, cu_k=30 * BUF + 64, tokens_q=tokens_q, dtype=dtype)
+    last_q, last_k = 10 * BUF + ((tokens_q - 1) * 128 + 127) * (2, 4)[1 - dtype], 20 * BUF + (11 * 64 + 63) * (2, 4)[1 - dtype]
+    need = ctypes.c_size_t()
+    assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(qk), ctypes.byref(need)) == 0
+    inputs = [10 * BUF, last_q // 4 * 4, 20 * BUF, last_k // 4 * 4, 30 * BUF, 30 * BUF + 8, 30 * BUF + 64, 30 * BUF + 72]
+    for at in inputs + [60 * BUF, 60 * BUF + need.value - 4]:
+        for name in ("q", "k"):
+            assert _smax_call(lib, handle, qk, **{**far, name: at}) == OVERLAP, (name, at)
+            assert _smax_call(lib, handle, qk, **{**far, "q": None, "k": None, name: at}) == OVERLAP
+    assert _smax_call(lib, handle, qk, **{**far, "q": 50 * BUF + 4}) == OVERLAP     # on the other output
+    for at in inputs:
+        assert _smax_call(lib, handle, qk, **{**far, "ws": at // 256 * 256}) == OVERLAP, at
+
+
+def test_smax_spans_that_no_memory_holds_are_refused(lib, handle):
+    for over in (dict(q_token=1 << 40, tokens_q=1 << 30), dict(k_token=1 << 40, tokens_k=1 << 30),
+                 dict(q_head=1 << 40, heads_q=65536)):
+        sz = ctypes.c_size_t()
+        assert _smax_call(lib, handle, _qk(**over), nbytes=1 << 40) == INVALID
+        assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(_qk(**over)), ctypes.byref(sz)) == INVALID
