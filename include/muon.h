@@ -63,7 +63,7 @@ typedef enum {
     MUON_ERR_INVALID_ARG = 1,        /* null pointer, bad size/stride/enum  */
     MUON_ERR_UNSUPPORTED_DEVICE = 2, /* not a gfx950 device, or bad ordinal */
     MUON_ERR_WORKSPACE = 3,          /* workspace null or smaller than required */
-    MUON_ERR_OVERLAP = 4,            /* param/grad/momentum ranges overlap  */
+    MUON_ERR_OVERLAP = 4,            /* ranges that the call writes overlap */
     MUON_ERR_HIP = 5,                /* a HIP runtime call failed           */
     MUON_ERR_UNALIGNED = 6,          /* pointer not aligned to its element  */
     MUON_ERR_SCRATCH = 7             /* larger than the fixed scratch of an allocation-free call */
@@ -325,7 +325,8 @@ muon_status muon_grad_clip(muon_handle h, const muon_grad* gs, int n, float max_
 
 /* muon_step_batched and adamw_step with every gradient multiplied by the
  * device float *grad_scale first (read when the step runs; the gradient
- * tensors are not modified).  grad_scale may not lie in the workspace. */
+ * tensors are not modified).  grad_scale may lie neither in the workspace nor
+ * in a tensor that the step writes (MUON_ERR_OVERLAP). */
 muon_status muon_step_batched_scaled(muon_handle h, const muon_matrix* mats, int n,
                                      const muon_hparams* hp, const float* grad_scale,
                                      void* workspace, size_t workspace_bytes, void* stream);

@@ -143,6 +143,22 @@ muon_status muon_workspace_size(muon_handle h, const muon_matrix* mats, int n,
 
 namespace {
 
+// Whether the scalar lies in a tensor that the step writes.
+bool written(const muon_matrix& m, const float* scalar) {
+    const Rect s = run_of(scalar, 4, false, 0);
+    return collide(s, rect_of(m.momentum, m.rows, m.cols, m.ld_mom, 4, true, 1)) ||
+           collide(s, rect_of(m.param, m.rows, m.cols, m.ld_param, elem_bytes(m.param_dtype), true, 1)) ||
+           (m.update_out && collide(s, rect_of(m.update_out, m.rows, m.cols, m.cols, 4, true, 1))) ||
+           (m.norm_out && collide(s, run_of(m.norm_out, 4, true, 1)));
+}
+bool written(const adamw_tensor& t, const float* scalar) {
+    if (t.numel == 0) return false;
+    const Rect s = run_of(scalar, 4, false, 0);
+    return collide(s, run_of(t.param, (size_t)t.numel * elem_bytes(t.param_dtype), true, 1)) ||
+           collide(s, run_of(t.exp_avg, (size_t)t.numel * 4, true, 1)) ||
+           collide(s, run_of(t.exp_avg_sq, (size_t)t.numel * 4, true, 1));
+}
+
 // One Muon step; gscale: null, or the device scalar that multiplies every
 // gradient.
 muon_status step_batched(muon_handle h, const muon_matrix* mats, int n, const muon_hparams* hp,
@@ -155,6 +171,10 @@ muon_status step_batched(muon_handle h, const muon_matrix* mats, int n, const mu
     muon_status st = make_plan(mats, n, hp, true, ws, h->cus_per_xcd, P);
     if (st != MUON_OK) return st;
     if (workspace_bytes < P.total) return MUON_ERR_WORKSPACE;
+    // blocks write momentum while others have yet to read the scale
+    if (gscale)
+        for (int i = 0; i < n; ++i)
+            if (written(mats[i], gscale)) return MUON_ERR_OVERLAP;
 
     DeviceGuard g(h->device);
     hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -401,6 +421,9 @@ muon_status adamw_step_scaled(muon_handle h, const adamw_tensor* ts, int n, cons
     if (reinterpret_cast<uintptr_t>(grad_scale) % 4) return MUON_ERR_UNALIGNED;
     muon_status st = check_adamw(ts, n, hp);
     if (st != MUON_OK) return st;
+    // blocks write the tensors while others have yet to read the scale
+    for (int i = 0; i < n; ++i)
+        if (written(ts[i], grad_scale)) return MUON_ERR_OVERLAP;
     DeviceGuard g(h->device);
     return hip_status(adamw_launch_all(h, ts, n, hp, grad_scale, reinterpret_cast<hipStream_t>(stream)));
 }

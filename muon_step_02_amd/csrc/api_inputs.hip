@@ -12,46 +12,6 @@ using namespace muon;
 
 namespace {
 
-// `rows` rows of `width` bytes, `stride` bytes apart.
-struct Rect {
-    uintptr_t lo, hi;
-    size_t width, stride;
-    bool write;
-    int owner;
-};
-
-Rect rect_of(const void* p, int64_t rows, int64_t cols, int64_t ld, size_t es, bool write, int owner) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    return Rect{b, b + (size_t)((rows - 1) * ld + cols) * es, (size_t)cols * es,
-                (size_t)(rows > 1 ? ld : cols) * es, write, owner};
-}
-
-// Whether two ranges share bytes.  Column blocks of one buffer (the same row
-// stride, disjoint columns) interleave without sharing any, and so does what
-// lies between a tensor's rows.
-bool collide(const Rect& a, const Rect& b) {
-    if (a.hi <= b.lo || b.hi <= a.lo) return false;
-    if (a.stride == b.stride) {
-        const Rect& f = a.lo <= b.lo ? a : b;
-        const Rect& s = a.lo <= b.lo ? b : a;
-        const size_t d = (s.lo - f.lo) % f.stride;
-        return d < f.width || d + s.width > f.stride;
-    }
-    if (a.width != a.stride && b.width != b.stride) return true;
-    // one of them is one run of bytes: against the other's rows
-    const Rect& run = a.width == a.stride ? a : b;
-    const Rect& r = a.width == a.stride ? b : a;
-    if (run.lo <= r.lo) return true;
-    const size_t d = (run.lo - r.lo) % r.stride;
-    const uintptr_t next = run.lo + (r.stride - d);  // the row behind run.lo
-    return d < r.width || (next < run.hi && next < r.hi);
-}
-
-Rect run_of(const void* p, size_t bytes, bool write, int owner) {
-    const uintptr_t b = reinterpret_cast<uintptr_t>(p);
-    return Rect{b, b + bytes, bytes, bytes, write, owner};
-}
-
 // Whether a written range shares bytes with any other range, one owner's
 // ranges among themselves excepted.  Sorts `r`.
 bool any_collision(Rect* r, int n) {

@@ -195,3 +195,25 @@ def test_two_handles_and_two_streams():
             assert torch.equal(t, b.state()[name]), name
     finally:
         mu.muon_destroy(b.h)
+
+
+def test_a_scale_beside_what_the_steps_write():
+    """Behind a parameter's last value, and in the padding of a momentum's rows:
+    it belongs to no tensor there."""
+    a, b = Step(7), Step(7)
+    for s in (a, b):
+        mu.muon_expert_grad_weight(s.h, s.dw, s.offsets, s.x, s.dy)
+    scale = torch.full((1,), 0.25, device=DEV)
+    p = torch.zeros(1001, device=DEV)
+    p[:1000], p[1000] = a.p, 0.25
+    mu.adamw_step_scaled(a.h, [mu.adamw_tensor(p[:1000], a.gp, a.m, a.v)], a.ahp, p[1000:])
+    mom = torch.zeros(N, K + 4, device=DEV)
+    mom[5, K + 1] = 0.25
+    mats = [mu.muon_matrix(a.W[0], a.G[0], mom[:, :K], a.O[0])]
+    mu.muon_step_batched_scaled(a.h, mats, a.hp, mom[5, K + 1:K + 2], a.ws)
+    mu.adamw_step_scaled(b.h, b.ts, b.ahp, scale)
+    mu.muon_step_batched_scaled(b.h, b.mats[:1], b.hp, scale, b.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(p[:1000], b.p) and torch.equal(a.m, b.m) and torch.equal(a.v, b.v)
+    assert torch.equal(a.W[0], b.W[0]) and torch.equal(mom[:, :K], b.M[0])
+    assert float(mom[5, K + 1]) == 0.25 and float(p[1000]) == 0.25

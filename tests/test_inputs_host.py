@@ -442,3 +442,23 @@ def test_smax_spans_that_no_memory_holds_are_refused(lib, handle):
         sz = ctypes.c_size_t()
         assert _smax_call(lib, handle, _qk(**over), nbytes=1 << 40) == INVALID
         assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(_qk(**over)), ctypes.byref(sz)) == INVALID
+
+
+def test_a_scale_in_what_a_step_writes_is_refused(lib, handle):
+    """4 x 8 weights, their momentum and outputs; AdamW tensors of 32 values."""
+    hp, ahp = mu.muon_hparams(lr=1e-3), mu.adamw_hparams(1e-3, 1)
+    m = mu.MuonMatrix(param=2 * BUF, grad=3 * BUF, momentum=4 * BUF, update_out=5 * BUF, norm_out=6 * BUF,
+                      rows=4, cols=8, ld_param=8, ld_grad=8, ld_mom=8)
+    other = mu.MuonMatrix(param=12 * BUF, grad=13 * BUF, momentum=14 * BUF, rows=4, cols=8, ld_param=8,
+                          ld_grad=8, ld_mom=8, param_dtype=1)
+    for mats in ((m, other), (other, m)):
+        arr = (mu.MuonMatrix * 2)(*mats)
+        for at in (2 * BUF, 2 * BUF + 124, 4 * BUF, 4 * BUF + 60, 5 * BUF + 4, 6 * BUF, 12 * BUF + 60, 14 * BUF + 124):
+            assert lib.muon_step_batched_scaled(handle, arr, 2, ctypes.byref(hp), at, 32 * BUF, 1 << 24,
+                                                None) == OVERLAP, at
+    t = mu.AdamwTensor(param=2 * BUF, grad=3 * BUF, exp_avg=4 * BUF, exp_avg_sq=5 * BUF, numel=32)
+    bf = mu.AdamwTensor(param=12 * BUF, grad=13 * BUF, exp_avg=14 * BUF, exp_avg_sq=15 * BUF, numel=32, param_dtype=1)
+    for ts in ((t, bf), (bf, t)):
+        arr = (mu.AdamwTensor * 2)(*ts)
+        for at in (2 * BUF, 2 * BUF + 124, 4 * BUF + 8, 5 * BUF + 64, 12 * BUF + 60, 14 * BUF, 15 * BUF + 124):
+            assert lib.adamw_step_scaled(handle, arr, 2, ctypes.byref(ahp), at, None) == OVERLAP, at
