@@ -268,6 +268,10 @@ Rect tokens_rect(const void* p, int64_t tokens, int64_t width, int64_t ld, int32
     return rect_of(p, tokens, width, ld, elem_bytes(dtype), write, 0);
 }
 
+// launch_expert finds out which tiles a call takes, and refuses the sizes whose
+// tiles no launch holds.
+muon_status expert_status(hipError_t e) { return e == hipErrorInvalidConfiguration ? MUON_ERR_INVALID_ARG : hip_status(e); }
+
 bool grid_fits(int64_t a, int64_t b, int64_t c) { return a * b <= INT32_MAX / (c > 0 ? c : 1); }
 
 muon_status expert_rows(ExpertOp op, muon_handle h, const muon_experts* ex, const int32_t* offsets,
@@ -301,7 +305,7 @@ muon_status expert_rows(ExpertOp op, muon_handle h, const muon_experts* ex, cons
     c.cols = (int32_t)ex->cols;
     c.bf16 = ex->dtype == MUON_BF16;
     DeviceGuard g(h->device);
-    return hip_status(launch_expert(op, c, ex->weights, reinterpret_cast<hipStream_t>(stream)));
+    return expert_status(launch_expert(op, c, ex->weights, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
@@ -369,7 +373,7 @@ muon_status muon_expert_grad_weight(muon_handle h, const muon_experts* grads, co
     c.out_bf16 = grads->dtype == MUON_BF16;
     c.accumulate = accumulate;
     DeviceGuard g(h->device);
-    return hip_status(launch_expert(kExpertGradWeight, c, grads->weights, reinterpret_cast<hipStream_t>(stream)));
+    return expert_status(launch_expert(kExpertGradWeight, c, grads->weights, reinterpret_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"
@@ -416,9 +420,11 @@ muon_status check_qk(const muon_qk* s, SmaxCall* c, int64_t* parts, muon_handle 
     c->causal = s->causal;
     c->scale = s->scale;
     const bool fast = smax_chunked(*c);
-    *parts = smax_plan(*c, 8 * h->cus_per_xcd, !fast);
-    *parts = std::max(*parts, smax_plan(*c, 8 * h->cus_per_xcd, fast));
-    return *parts > INT32_MAX ? MUON_ERR_INVALID_ARG : MUON_OK;
+    const int64_t other = smax_plan(*c, 8 * h->cus_per_xcd, !fast);
+    const int64_t taken = smax_plan(*c, 8 * h->cus_per_xcd, fast);
+    *parts = std::max(other, taken);
+    // a launch of 256 threads a part holds fewer than 2^32
+    return *parts > INT32_MAX || taken > UINT32_MAX / 256 ? MUON_ERR_INVALID_ARG : MUON_OK;
 }
 
 // Outputs and workspace share no memory with anything else of the call: blocks

@@ -454,6 +454,9 @@ bool mid_tiles(int64_t big, int64_t mid) {
     return tm < tb;
 }
 
+// A launch holds fewer than 2^32 threads.
+bool launch_fits(int64_t blocks, int threads) { return blocks * threads <= UINT32_MAX; }
+
 template <int CAP>
 hipError_t launch_bf16(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& w, hipStream_t st) {
     // dealt_tile covers every tile where the grid holds at least as many
@@ -462,6 +465,7 @@ hipError_t launch_bf16(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& 
     if (op == kExpertGradWeight) {
         const int mt = (c.rows + kWM - 1) / kWM, nt = (c.cols + kWN - 1) / kWN;
         const unsigned n = grid((int64_t)c.experts * mt * nt);
+        if (!launch_fits(n, 256)) return hipErrorInvalidConfiguration;
         if (c.out_bf16) {
             if (c.accumulate)
                 expert_weight_kernel<CAP, true, true><<<n, 256, 0, st>>>(c, w, mt, nt);
@@ -486,6 +490,7 @@ hipError_t launch_bf16(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& 
         const int64_t mt = c.tokens / bm + (c.tokens < c.experts ? c.tokens : c.experts);
         const int nt = (N + bn - 1) / bn;
         const unsigned n = grid(mt * nt);
+        if (!launch_fits(n, few ? 128 : mid ? 256 : 512)) return hipErrorInvalidConfiguration;
         if (op == kExpertForward) {
             if (few)
                 expert_few_kernel<kExpertForward, CAP><<<n, 128, 0, st>>>(c, w, nt);
@@ -561,6 +566,8 @@ template <int T, int CAP>
 hipError_t launch_loose(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& w, hipStream_t st) {
     const int64_t nr = (c.rows + T - 1) / T, nc = (c.cols + T - 1) / T;
     const int64_t mt = c.tokens / T + (c.tokens < c.experts ? c.tokens : c.experts);
+    if (!launch_fits(op == kExpertGradWeight ? c.experts * nr * nc : mt * (op == kExpertForward ? nr : nc), 256))
+        return hipErrorInvalidConfiguration;
     if (op == kExpertGradWeight) {
         const unsigned n = (unsigned)(c.experts * nr * nc);
         if (c.out_bf16) {
@@ -587,12 +594,13 @@ hipError_t launch_any(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& w
     const int64_t nr = (c.rows + T - 1) / T, nc = (c.cols + T - 1) / T;
     // at most this many row tiles: every group may end in a ragged one
     const int64_t mt = c.tokens / T + (c.tokens < c.experts ? c.tokens : c.experts);
+    const int64_t tiles = op == kExpertGradWeight ? c.experts * nr * nc : mt * (op == kExpertForward ? nr : nc);
     if (c.bf16) {
         // 128 x 128 tiles where they fill the chip twice (4 experts of 2049 x
         // 4097, 1024 rows: 227 us), else 64 x 64
-        const int64_t tiles = op == kExpertGradWeight ? c.experts * nr * nc : mt * (op == kExpertForward ? nr : nc);
         return tiles >= 4 * 1024 ? launch_loose<128, CAP>(op, c, w, st) : launch_loose<64, CAP>(op, c, w, st);
     }
+    if (!launch_fits(tiles, 256)) return hipErrorInvalidConfiguration;
     if (op == kExpertGradWeight)
         expert_weight_any_kernel<CAP><<<(unsigned)(c.experts * nr * nc), 256, 0, st>>>(c, w, (int)nr, (int)nc);
     else if (op == kExpertForward)

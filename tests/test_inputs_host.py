@@ -462,3 +462,18 @@ def test_a_scale_in_what_a_step_writes_is_refused(lib, handle):
         arr = (mu.AdamwTensor * 2)(*ts)
         for at in (2 * BUF, 2 * BUF + 124, 4 * BUF + 8, 5 * BUF + 64, 12 * BUF + 60, 14 * BUF, 15 * BUF + 124):
             assert lib.adamw_step_scaled(handle, arr, 2, ctypes.byref(ahp), at, None) == OVERLAP, at
+
+
+def test_more_threads_than_a_launch_holds_are_refused(lib, handle):
+    """A launch takes fewer than 2^32 threads: ragged tiles of many groups over
+    very wide outputs pass that within the sizes each argument may have."""
+    wide = 1 << 20
+    for over, tokens in ((dict(cols=8, ld=8, dtype=1), 32768), (dict(cols=8, ld=9, dtype=1), 1 << 17),
+                         (dict(cols=1, ld=1, dtype=0), 1024)):
+        ex = _experts(n=1024, at=1 << 40, step=1 << 25, rows=wide, **over)
+        assert _rows_call(lib, handle, ex, x=BUF, ld_x=8, offsets=8 * BUF, y=1 << 44, ld_y=wide, tokens=tokens) == INVALID
+    qk = _qk(q=1 << 40, k=1 << 44, heads_q=128, q_token=128 * 32, tokens_q=1 << 20, tokens_k=1 << 20,
+             sequences=1 << 20, cu_q=8 * BUF, cu_k=16 * BUF)
+    sz = ctypes.c_size_t()
+    assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(qk), ctypes.byref(sz)) == INVALID
+    assert _smax_call(lib, handle, qk, q=32 * BUF, k=33 * BUF, ws=1 << 46, nbytes=1 << 40) == INVALID
