@@ -358,3 +358,34 @@ def test_wide_tiles(k):
     sizes = [225, 193, 200, 161, 100, 33, 256, 1, 289]
     Layer(sizes, 4104, k, BF16, seed=k).check()
     Layer(sizes, k, 4104, BF16, seed=k + 1, pad=8).check()
+
+
+# bf16 rows that do not start on 16 bytes, enough of them for the 128 x 128 tiles
+# that go through registers: taken from 4096 tiles of 64 x 64 on.  Rows: 8000 / 64
+# + 4 groups = 129 tiles by at least 32; weights: 4 experts by 32 x 33.
+@pytest.mark.parametrize("grad_dtype", [BF16, F32], ids=["bf16", "bf16 to fp32"])
+@pytest.mark.parametrize("rows,cols,pad,shift", [(2049, 2057, 0, 0), (2048, 2112, 1, 0), (2048, 2112, 8, 3)],
+                         ids=["odd widths", "odd leading dimensions", "odd starts"])
+def test_large_products_at_other_alignments(rows, cols, pad, shift, grad_dtype):
+    Layer([3000, 0, 4097, 903], rows, cols, BF16, grad_dtype=grad_dtype, pad=pad, shift=shift, seed=rows + pad).check()
+
+
+def test_large_products_at_other_alignments_read_no_other_group():
+    """As the test of non-finite values above, for 128 x 128 tiles; rows of a
+    group end inside a tile and inside a chunk of 8."""
+    sizes, rows, cols = [3001, 4097, 902], 2049, 2057
+    a, b = (Layer(sizes, rows, cols, BF16, grad_dtype=F32, seed=9) for _ in range(2))
+    for t in (b.x, b.dy):
+        t[3001:7098] = float("nan")
+        t[8000:] = float("nan")
+    b.w[1].fill_(float("nan"))
+    h = Handle.get()
+    for L in (a, b):
+        ex, gr = mu.muon_experts(L.w), mu.muon_experts(L.dw)
+        mu.muon_expert_forward(h, ex, L.offsets, L.x, L.y)
+        mu.muon_expert_grad_input(h, ex, L.offsets, L.dy, L.dx)
+        mu.muon_expert_grad_weight(h, gr, L.offsets, L.x, L.dy)
+    for got, want in ((b.y, a.y), (b.dx, a.dx)):
+        assert torch.equal(got[:3001], want[:3001]) and torch.equal(got[7098:], want[7098:])
+    for e in (0, 2):
+        assert torch.equal(a.dw[e], b.dw[e])
