@@ -282,3 +282,35 @@ def test_binding_refuses():
     with pytest.raises(mu.MuonError) as e:
         mu.muon_qk_smax(h, q[:, :3], k, cu, cu, out[:3], ws)
     assert e.value.status == 1
+
+
+# Sequences of 512 queries and more on average take tiles of 256 queries, every
+# head size its own kernel: ragged ends, more and fewer keys than queries, heads
+# that divide by 8 (dealt to the XCDs) and heads that do not.
+@pytest.mark.parametrize("heads,kv", [(4, 2), (8, 8)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dim", [8, 64, 80, 96, 128, 160, 192, 200, 256])
+def test_long_sequences_of_every_head_size(dim, causal, heads, kv):
+    nq, nk = [700, 1, 1301, 613], [700, 40, 1400, 333]
+    _check_whole(_ints(27, sum(nq), heads, dim, BF16), _ints(28, sum(nk), kv, dim, BF16), nq, nk, causal)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_long_sequences_read_no_masked_value(dim):
+    """NaN in every key behind the last one a query sees, and behind the
+    sequences: none may reach a maximum."""
+    n, more = 600, 64
+    q, k = _ints(29, n, 2, dim, BF16), _ints(30, n + more, 2, dim, BF16)
+    at, cu = _cu([n])
+    want = _call(q, k[:n], cu, cu, 1.0, True)[0]
+    k[n:] = float("nan")
+    assert torch.equal(_call(q, k, cu, cu, 1.0, True)[0], want)
+    assert torch.equal(want, _reference(q, k[:n], at, at, 1.0, True)[0].float())
+    # the last query alone sees the last key
+    k[n - 1] = float("nan")
+    assert bool(torch.isnan(_call(q, k, cu, cu, 1.0, True)[0]).all())
+    q[n - 1:] = float("nan")
+    cu_q = torch.tensor([0, n - 1], dtype=torch.int32, device=DEV)
+    cu_k = torch.tensor([0, n - 1], dtype=torch.int32, device=DEV)
+    got = _call(q, k, cu_q, cu_k, 1.0, True)[0]
+    assert torch.equal(got, _reference(q, k, [0, n - 1], [0, n - 1], 1.0, True)[0].float())
