@@ -248,3 +248,11 @@ def test_scalars_between_the_rows_of_a_gradient():
     _check_norm(buf[0, 128], norm)
     assert abs(float(buf[7, 135]) - scale) <= NORM_TOL * scale
     _check_outs([before], [g], scale)
+
+
+# More tensors than a launch holds and more chunks than there are blocks (fp32
+# 23 + 17 + 16 chunks of 16 KB each hundred times, bf16 12 + 9 + 8): the blocks
+# go to the launches in proportion, and so do their partial sums.
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_many_tensors_of_many_chunks(dtype):
+    test_norm_and_clip([(130, 700, 4), 65537, (64, 1024, 0)] * 100, dtype)
