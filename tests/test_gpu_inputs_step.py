@@ -10,7 +10,7 @@ import torch
 import muon_step_02_amd as mu
 import oracle
 import synth
-from harness import Handle, TOL_O_BF16, TOL_STATE, f64, hp_from, oracle_kwargs, recipe_floor_output, relF
+from harness import Handle, TOL_O_BF16, TOL_O_F32, TOL_STATE, f64, hp_from, oracle_kwargs, recipe_floor_output, relF
 
 pytestmark = pytest.mark.gpu
 
@@ -217,3 +217,43 @@ def test_a_scale_beside_what_the_steps_write():
     assert torch.equal(p[:1000], b.p) and torch.equal(a.m, b.m) and torch.equal(a.v, b.v)
     assert torch.equal(a.W[0], b.W[0]) and torch.equal(mom[:, :K], b.M[0])
     assert float(mom[5, K + 1]) == 0.25 and float(p[1000]) == 0.25
+
+
+@pytest.mark.parametrize("ns_dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("grad_dtype", [torch.float32, torch.bfloat16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("pad", [0, 4, 3])
+def test_scaled_steps_of_every_layout(pad, grad_dtype, ns_dtype):
+    """Wide and tall matrices, padded rows that vector accesses fit and that they
+    do not: a scaled step against the oracle's step on scaled gradients."""
+    g = torch.Generator(device=DEV).manual_seed(11)
+    scale = torch.full((1,), 0.3, device=DEV)
+    s64 = float(scale.double())
+    hp = hp_from(synth.MUON_DEFAULT, ns_dtype=ns_dtype)
+    shapes, mats, held = [(96, 200), (200, 96), (160, 416), (416, 160), (8, 24)], [], []
+
+    def tensor(r, c, dtype=torch.float32, std=1.0):
+        return (torch.randn(r, c + pad, generator=g, device=DEV) * std).to(dtype)[:, :c]
+
+    for r, c in shapes:
+        W, G, M = tensor(r, c, std=0.02), tensor(r, c, grad_dtype), tensor(r, c, std=0.1)
+        O = torch.zeros(r, c, device=DEV)
+        held.append((W, G, M, O, f64(W), f64(G), f64(M)))
+        mats.append(mu.muon_matrix(W, G, M, O))
+    h = Handle.get()
+    ws = torch.empty(mu.muon_workspace_size(h, mats, hp), dtype=torch.uint8, device=DEV)
+    mu.muon_step_batched_scaled(h, mats, hp, scale, ws)
+    n = 4097 + pad
+    p, pg = torch.randn(n + 1, generator=g, device=DEV)[1:], torch.randn(n + 1, generator=g, device=DEV).to(grad_dtype)[1:]
+    p0 = f64(p)
+    m, v = torch.zeros(n, device=DEV), torch.zeros(n, device=DEV)
+    mu.adamw_step_scaled(h, [mu.adamw_tensor(p, pg, m, v)], mu.adamw_hparams(step=1, **synth.ADAMW_DEFAULT), scale)
+    torch.cuda.synchronize()
+    kw = oracle_kwargs(synth.MUON_DEFAULT)
+    for W, G, M, O, W0, G0, M0 in held:
+        Wr, Mr, Or = oracle.muon_matrix_step(W0, G0 * s64, M0, **kw)
+        # three roundings of 2^-24 beside the unscaled step's
+        assert relF(f64(M), Mr) <= TOL_STATE, W.shape
+        # 8 x 24 runs in fp32 in either mode
+        assert relF(f64(O), Or) <= (TOL_O_F32 if ns_dtype == "fp32" else TOL_O_BF16), W.shape
+    th, mr, vr = oracle.adamw_tensor_step(p0, f64(pg) * s64, np.zeros(n), np.zeros(n), step=1, **synth.ADAMW_DEFAULT)
+    assert relF(f64(m), mr) <= TOL_STATE and relF(f64(v), vr) <= TOL_STATE and relF(f64(p), th) <= TOL_STATE
