@@ -256,3 +256,17 @@ def test_scalars_between_the_rows_of_a_gradient():
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_many_tensors_of_many_chunks(dtype):
     test_norm_and_clip([(130, 700, 4), 65537, (64, 1024, 0)] * 100, dtype)
+
+
+@pytest.mark.parametrize("shapes", [[1 << 23], [70000] * 257, [1] * 600, [(130, 700, 4), 65537] * 300],
+                         ids=["one tensor", "257 tensors", "600 values", "600 tensors"])
+def test_the_workspace_is_as_large_as_its_size_says(shapes):
+    h = Handle.get()
+    grads, _ = _make(shapes, torch.float32, 6)
+    plan = [mu.muon_grad(g) for g in grads]
+    need = mu.muon_grad_workspace_size(h, plan)
+    buf = torch.full((need + (1 << 16),), 0xA5, dtype=torch.uint8, device=DEV)
+    norm = torch.zeros(1, device=DEV)
+    mu.muon_grad_norm(h, plan, 1.0, buf[:need], norm_out=norm)
+    _check_norm(norm, _reference(grads, 1.0)[0])
+    assert bool((buf[need:] == 0xA5).all())

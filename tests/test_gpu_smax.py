@@ -314,3 +314,21 @@ def test_long_sequences_read_no_masked_value(dim):
     cu_k = torch.tensor([0, n - 1], dtype=torch.int32, device=DEV)
     got = _call(q, k, cu_q, cu_k, 1.0, True)[0]
     assert torch.equal(got, _reference(q, k, [0, n - 1], [0, n - 1], 1.0, True)[0].float())
+
+
+@pytest.mark.parametrize("dtype,dim", [(BF16, 64), (BF16, 63), (F32, 64)])
+@pytest.mark.parametrize("nq,nk", [([1], [9000]), ([70, 1, 0, 3], [4000, 1, 5, 70]), ([129] * 5, [129] * 5),
+                                   ([1500], [1500]), ([1] * 40, [2] * 40)])
+def test_the_workspace_is_as_large_as_its_size_says(nq, nk, dtype, dim):
+    """Nothing behind it is written: few queries, whose keys are split over
+    workgroups, and many short sequences, each with a ragged tile."""
+    h = Handle.get()
+    q, k = _ints(31, sum(nq), 6, dim, dtype), _ints(32, sum(nk), 2, dim, dtype)
+    at_q, cu_q = _cu(nq)
+    at_k, cu_k = _cu(nk)
+    need = mu.muon_qk_smax_workspace_size(h, q, k, cu_q)
+    buf = torch.full((need + (1 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+    sq = torch.zeros(6, device=DEV)
+    mu.muon_qk_smax(h, q, k, cu_q, cu_k, sq, buf[:need], scale=1.0)
+    assert torch.equal(sq, _reference(q, k, at_q, at_k, 1.0, True)[0].float())
+    assert bool((buf[need:] == 0xA5).all())

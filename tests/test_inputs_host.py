@@ -477,3 +477,29 @@ def test_more_threads_than_a_launch_holds_are_refused(lib, handle):
     sz = ctypes.c_size_t()
     assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(qk), ctypes.byref(sz)) == INVALID
     assert _smax_call(lib, handle, qk, q=32 * BUF, k=33 * BUF, ws=1 << 46, nbytes=1 << 40) == INVALID
+
+
+# ---- workspaces -----------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [1, 16, 17, 256, 257, 512, 513, 5000])
+def test_grad_workspace_holds_a_sum_per_block(lib, handle, n):
+    """2048 blocks in proportion to the chunks, and one more for every launch of
+    256 tensors at most: a 64-bit sum each."""
+    sz = ctypes.c_size_t()
+    arr = (mu.MuonGrad * n)(*[_grad()] * n)
+    assert lib.muon_grad_workspace_size(handle, arr, n, ctypes.byref(sz)) == 0
+    assert sz.value >= 8 * (2048 + (n + 255) // 256)
+
+
+@pytest.mark.parametrize("tq,seqs", [(1, 1), (63, 2), (64, 1), (65, 65), (5000, 33), (9000, 3), (40, 1000), (0, 5)])
+@pytest.mark.parametrize("heads", [1, 12, 64])
+@pytest.mark.parametrize("dtype,dim", [(1, 32), (1, 33), (0, 32)])
+def test_smax_workspace_holds_a_maximum_per_tile(lib, handle, tq, seqs, heads, dtype, dim):
+    """Every sequence may end in a ragged tile, of 64 queries in the kernel for
+    any type and of 128 or 256 in the others; with alignment the kernel may
+    change while the size does not."""
+    sz = ctypes.c_size_t()
+    qk = _qk(tokens_q=tq, sequences=seqs, heads_q=heads, heads_k=1, head_dim=dim, q_head=dim, k_head=dim,
+             q_token=heads * dim, k_token=dim, dtype=dtype)
+    assert lib.muon_qk_smax_workspace_size(handle, ctypes.byref(qk), ctypes.byref(sz)) == 0
+    assert sz.value >= 4 * heads * (tq // 64 + min(seqs, tq))
