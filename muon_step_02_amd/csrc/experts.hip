@@ -134,8 +134,7 @@ __global__ __launch_bounds__(256) void expert_weight_any_kernel(ExpertCall c, Ex
 
 // ---- bf16 on the matrix cores ------------------------------------------------
 
-// Row tile `mt` as find_group, and the group's number of row tiles before it;
-// total: row tiles of all groups.
+// Row tiles of all groups.
 template <int BM>
 __device__ __forceinline__ int count_tiles(const ExpertCall& c) {
     const int lane = threadIdx.x & 63;
@@ -225,8 +224,7 @@ __device__ __forceinline__ void rows_product(const ExpertCall& c, const RowsTile
     else
         bf::product<C>(acc, t.p, t.q, t.K, st);
     const int64_t ld = c.ld_c;
-    bf::for_each_chunk<C>(acc, reinterpret_cast<float*>(st.q[0]), t.rows, [](int) {},
-                          [&](int, int, int r, int c8, const float* v) {
+    bf::for_each_chunk<C>(acc, reinterpret_cast<float*>(st.q[0]), t.rows, [&](int r, int c8, const float* v) {
         if (r < t.rows && c8 < t.cols) gst(reinterpret_cast<uint4*>(t.out + r * ld + c8), bf::pack8(v));
     });
 }
@@ -398,7 +396,7 @@ constexpr int kWM = 128, kWN = 256;
 
 template <int CAP, bool OBF, bool ADD>
 __global__ __launch_bounds__(256, 2) void expert_weight_kernel(ExpertCall c, ExpertPtrs<CAP> w, int mtiles, int ntiles) {
-    using C = bf::Cfg<kWM, kWN, 2, 2, true, true, 32, 3, 16>;
+    using C = bf::Cfg<kWM, kWN, 2, 2, true, true, 32, 3>;
     constexpr int SP = kWM * 32, SQ = kWN * 32;
     __shared__ __attribute__((aligned(1024))) uint16_t lp0[SP], lq0[SQ], lp1[SP], lq1[SQ], lp2[SP], lq2[SQ];
     const bf::Stages<3> st{{lp0, lp1, lp2}, {lq0, lq1, lq2}};

@@ -28,8 +28,7 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) void lds_void;
 
 // PKM, QKM: the operand is stored k-major.  BK: k per slab; NS: LDS stages.
-// RB: rows of an epilogue band, 32 or 16 (RB x BN floats fit one stage array).
-template <int BM_, int BN_, int WM_, int WN_, bool PKM_, bool QKM_, int BK_ = 64, int NS_ = 2, int RB_ = 32>
+template <int BM_, int BN_, int WM_, int WN_, bool PKM_, bool QKM_, int BK_ = 64, int NS_ = 2>
 struct Cfg {
     static constexpr int BK = BK_, NS = NS_;
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
@@ -37,13 +36,12 @@ struct Cfg {
     static constexpr int NW = WM * WN, NT = 64 * NW;
     static constexpr int TM = BM / WM, TN = BN / WN;
     static constexpr int FM = TM / 32, FN = TN / 32;
-    static constexpr int RB = RB_;
     static constexpr int CH = BK / 8;                          // 16-byte chunks of a K-contiguous row
     static constexpr int LPS = (BM + BN) * BK / 512 / NW;      // copies of a wave and stage
     static_assert(FM >= 1 && FN >= 1 && BM % 32 == 0 && BN % 64 == 0, "32 x 32 blocks per wave");
     static_assert(BM * BK / 512 % NW == 0 && BN * BK / 512 % NW == 0, "slab copies split evenly over the waves");
-    static_assert((BK == 32 || BK == 64) && NS >= 2 && NS <= 5 && (RB == 16 || RB == 32), "");
-    static_assert(RB * BN % (8 * NT) == 0, "epilogue chunks split evenly over the threads");
+    static_assert((BK == 32 || BK == 64) && NS >= 2 && NS <= 5, "");
+    static_assert(32 * BN % (8 * NT) == 0, "epilogue chunks split evenly over the threads");
 };
 
 // One operand of a tile.  K-contiguous: row i at base + i * ld, `bytes` from
@@ -480,7 +478,7 @@ __device__ __forceinline__ void product_any(f32x16 (&acc)[C::FM][C::FN], const A
     }
 }
 
-// Epilogue band (RB rows in fp32, in LDS): column c of row r at
+// Epilogue band (32 rows in fp32, in LDS): column c of row r at
 // c ^ ((r & 4) << 3) ^ ((r >> 3) << 4), so that the two half-waves of an
 // accumulator store (rows r and r + 4) lie 32 banks apart.
 template <class C>
@@ -488,52 +486,36 @@ __device__ __forceinline__ int band_at(int r, int c) {
     return r * C::BN + (c ^ ((r & 4) << 3) ^ ((r >> 3) << 4));
 }
 
-// Chunks of 8 columns that a thread stores per band, and the row and column of
-// its chunk q in band b.
-template <class C>
-constexpr int chunks_per_band() { return C::RB * C::BN / 8 / C::NT; }
-template <class C>
-__device__ __forceinline__ int chunk_row(int b, int q) {
-    return b * C::RB + (q * C::NT + threadIdx.x) / (C::BN / 8);
-}
-template <class C>
-__device__ __forceinline__ int chunk_col(int q) {
-    return (q * C::NT + threadIdx.x) % (C::BN / 8) * 8;
-}
-
-// Passes the tile row band by row band through LDS (`band`, RB x BN floats):
-// put(b, q, row, column, values) for chunk q of band b.  ahead(b) is called
-// before band b is put: loads for band b + 1 belong there.
-template <class C, class A, class F>
-__device__ __forceinline__ void for_each_chunk(const f32x16 (&acc)[C::FM][C::FN], float* band, int rows,
-                                               A&& ahead, F&& put) {
+// Passes the tile through LDS (`band`, 32 x BN floats) in bands of 32 rows:
+// put(row, column, values) for every chunk of 8 columns.
+template <class C, class F>
+__device__ __forceinline__ void for_each_chunk(const f32x16 (&acc)[C::FM][C::FN], float* band, int rows, F&& put) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int wm = wave / C::WN, wn = wave % C::WN;
 #pragma unroll
-    for (int b = 0; b < C::BM / C::RB; ++b) {
-        if (b * C::RB >= rows) break;  // uniform
-        ahead(b);
+    for (int b = 0; b < C::BM / 32; ++b) {
+        if (b * 32 >= rows) break;  // uniform
         __syncthreads();
-        constexpr int H = 32 / C::RB;  // bands of a block of 32 rows: 8 registers each of two
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
-            if (wm * C::TM + i * 32 == b / H * 32) {
+            if (wm * C::TM + i * 32 == b * 32) {
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-                    for (int r = b % H * (16 / H); r < b % H * (16 / H) + 16 / H; ++r)
-                        band[band_at<C>((8 * (r >> 2) + 4 * (lane >> 5) + (r & 3)) % C::RB,
+                    for (int r = 0; r < 16; ++r)
+                        band[band_at<C>(8 * (r >> 2) + 4 * (lane >> 5) + (r & 3),
                                         wn * C::TN + j * 32 + (lane & 31))] = acc[i][j][r];
             }
         }
         __syncthreads();
 #pragma unroll
-        for (int q = 0; q < chunks_per_band<C>(); ++q) {
-            const int rr = chunk_row<C>(0, q), c8 = chunk_col<C>(q);
+        for (int q = 0; q < 32 * C::BN / 8 / C::NT; ++q) {
+            const unsigned ch = q * C::NT + threadIdx.x;
+            const int rr = ch / (C::BN / 8), c8 = ch % (C::BN / 8) * 8;
             const float4 a0 = *reinterpret_cast<const float4*>(band + band_at<C>(rr, c8));
             const float4 a1 = *reinterpret_cast<const float4*>(band + band_at<C>(rr, c8) + 4);
             const float v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            put(b, q, b * C::RB + rr, c8, v);
+            put(b * 32 + rr, c8, v);
         }
     }
     __syncthreads();
@@ -542,7 +524,8 @@ __device__ __forceinline__ void for_each_chunk(const f32x16 (&acc)[C::FM][C::FN]
 // The tile by waves, without a barrier: each wave passes its own rows through
 // `mine` (16 x TN floats of LDS), 16 rows at a time, and gets them back four
 // columns a lane, a row's TN columns side by side.  put(b, q, row, column,
-// values) for piece q of band b; ahead(b) as for for_each_chunk.
+// values) for piece q of band b.  ahead(b) is called before band b is put:
+// loads for band b + 1 belong there.
 template <class C>
 constexpr int wave_pieces() { return 16 * C::TN / 256; }
 template <class C>
