@@ -132,7 +132,7 @@ class MuonGrad(ctypes.Structure):
         ("grad_dtype", ctypes.c_int32),
         ("out_dtype", ctypes.c_int32),
     ]
-    _device = None  # of the tensors it was made of (muon_grad)
+    _index = None  # device of the tensors it was made of (muon_grad; -1: no GPU)
 
 
 class MuonExperts(ctypes.Structure):
@@ -440,9 +440,9 @@ def _stream_on(stream, device, h):
 
 
 def _scalar(t, what):
-    import torch
     if t is None:
         return None
+    import torch
     if t.dtype != torch.float32 or t.numel() != 1:
         raise ValueError("%s must be one float32" % what)
     return t.data_ptr()
@@ -451,7 +451,7 @@ def _scalar(t, what):
 def _nbytes(workspace):
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    return workspace.numel() * workspace.element_size()
+    return workspace.nbytes
 
 
 def _int32(t, what):
@@ -509,7 +509,7 @@ def muon_grad(grad, out=None):
                 raise ValueError("grad and out layouts differ")
             g.rows, g.cols, g.ld_grad, old = 1, grad.numel(), grad.numel(), grad.numel()
         g.out, g.ld_out, g.out_dtype = out.data_ptr(), old, _dt(out)
-    g._device = grad.device
+    g._index = grad.get_device()
     g._keepalive = (grad, out)
     return g
 
@@ -526,9 +526,10 @@ def _grad_call(name, h, grads, max_norm, workspace, norm_out, scale_out, stream)
     dev = _same_device(workspace, norm_out, scale_out)
     arr = grads
     if not isinstance(grads, ctypes.Array):  # (whose structures have lost their tensors)
+        here = dev.index
         for g in grads:
-            if g._device is not None and g._device != dev:
-                raise ValueError("a gradient is on %s, the workspace on %s" % (g._device, dev))
+            if g._index != here and g._index is not None:
+                raise ValueError("a gradient is on %s, the workspace on %s" % (g._keepalive[0].device, dev))
         arr = (MuonGrad * len(grads))(*grads)
     _check(getattr(load(), name)(h, arr, len(arr), float(max_norm), _scalar(norm_out, "norm_out"),
                                  _scalar(scale_out, "scale_out"), workspace.data_ptr(),

@@ -304,6 +304,9 @@ class _On:
             self._t = torch.zeros(1024, dtype=dtype).as_strided(shape, stride)
         self.device = torch.device(device)
 
+    def get_device(self):
+        return -1 if self.device.index is None else self.device.index
+
     def __getattr__(self, name):
         return getattr(self._t, name)
 
