@@ -69,8 +69,9 @@ __device__ __forceinline__ bool find_group(const ExpertCall& c, int mt, Group& g
 // ---- fp32 of any alignment and size: 64 x 64 tiles -------------------------
 //
 // Bound by the fp32 matrix cores: 4 experts of 2049 x 4097 with 1024 rows 93
-// TFLOP/s (the library's fp32 product 154 at 8192^3); a call of few tiles by
-// the 0.45 us of matrix work that a tile has in each 32-deep slab.
+// TFLOP/s forward, 97 and 101 back (the library's fp32 product 154 at 8192^3); a
+// call of few tiles by the 0.45 us of matrix work that a tile has in each 32-deep
+// slab: 2 experts of 2613 x 3776 with 8 rows forward 126 us, 3776 x 2613 back 206.
 
 // A tile of the result, one value at a time: rounded once, from the fp32 sum.
 // Old values are loaded all before the first store: a load behind a store
@@ -389,9 +390,13 @@ __device__ __forceinline__ void store_result(const bf::f32x16 (&acc)[C::FM][C::F
 // unit: a group's rows are a short K, so reading and writing dW is most of
 // the traffic, and one workgroup does it while the other multiplies.  With
 // accumulate the old values of a band are loaded one band ahead.  64 experts of
-// 2048 x 7168 with 512 rows each, added to fp32: 1.95 ms (1.47 with 64 rows,
+// 2048 x 7168 with 512 rows each, added to fp32: 1.93 ms (1.47 with 64 rows,
 // where reading and writing dW is all; 256 x 256 tiles of eight waves 2.04,
-// 128 x 128 tiles 2.11, dW in 128-byte pieces from the accumulators 2.04).
+// 128 x 128 tiles 2.11, dW in 128-byte pieces from the accumulators 2.04);
+// written, 1.52 ms in fp32 and 1.21 in bf16: the products (0.82 at the library's
+// rate) and the stores of dW overlap in part only.  A workgroup walks all rows
+// of its group: few tiles with many rows leave compute units idle (one expert of
+// 128 x 256 with 32768 rows is one workgroup and 325 us).
 constexpr int kWM = 128, kWN = 256;
 
 template <int CAP, bool OBF, bool ADD>
@@ -439,9 +444,10 @@ bool chunked(ExpertOp op, const ExpertCall& c, const void* const* w) {
 }
 
 // Whether 128 x 128 tiles take less time than 256 x 256 ones: in hundredths of
-// a microsecond a slab, a round of 256 big tiles takes 110, and 8 in all go to
-// the longer start; a round of 512 small ones, two a compute unit, 115, of up
-// to 256 76.  Measured, big and small: 8 experts of 1024 x 1024, 512 rows each
+// a microsecond for each slab of K, a round of 256 big tiles takes 110, and the
+// launch 8 more for their longer start (in proportion to K as the rest is, over
+// the 16 to 112 slabs measured); a round of 512 small ones, two a compute unit,
+// 115, of up to 256 76.  Measured, big and small: 8 experts of 1024 x 1024, 512 rows each
 // (64 and 256 tiles) 26.0 and 16.0 us; 16 of 2048 x 2048, 256 rows (128 and
 // 512) 41.9 and 41.4; 64 of 2048 x 7168, 128 rows (512 and 1024) 359 and 390; 8
 // of 2056 outputs, 512 rows, K = 1000 (144 and 544) 29.0 and 40.9.
@@ -513,7 +519,9 @@ hipError_t launch_bf16(ExpertOp op, const ExpertCall& c, const ExpertPtrs<CAP>& 
 // T x T tiles of four waves through registers; blocks as in the fp32 kernels.
 // Bound by the registers' way into LDS and by value-aligned accesses: 8 experts
 // of 1001 x 2057, 512 rows each, forward 53 us (317 TFLOP/s; 34 us at 1000 x
-// 2056 on the kernels above), 2 experts of 2613 x 3776 with 8 rows 56 us.
+// 2056 on the kernels above), input gradient 75, weight gradient 92; 4 of 2049 x
+// 4097, 1024 rows each, 228, 248 and 245 us; 2 experts of 2613 x 3776 with 8 rows
+// forward 56 us, input gradient of 3777 x 2613 153.
 template <ExpertOp OP, int T, int CAP>
 __global__ __launch_bounds__(256) void expert_rows_loose_kernel(ExpertCall c, ExpertPtrs<CAP> w, int ntiles) {
     constexpr bool QKM = OP == kExpertGradInput;

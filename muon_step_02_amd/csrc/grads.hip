@@ -17,11 +17,14 @@
 // repeatable: block b takes chunks b, b + blocks, ... of the group.
 //
 // Measured: the norm of 192 fp32 gradients of 2048 x 7168 (11.3 GB) 1.81-1.86
-// ms, 6.1-6.2 TB/s, where a large in-place multiplication moves 5.9 TB/s; 470
-// MB of bf16 5.3-5.7 TB/s at any row padding.  The clip of 17 M fp32 values
-// (67 MB, the second read from the memory-side cache) 13 + 25 us; of 235 M bf16
-// values to fp32 112 + 252 us (5.6 TB/s in the second pass).  Four vectors of
-// 1024 values: 5 us in one workgroup, launch latency and two dependent loads.
+// ms, 6.1-6.2 TB/s, where a large in-place multiplication moves 5.9 TB/s; the
+// norm of 470 MB of bf16, at any row padding, 82-87 us, 5.4-5.7 TB/s.  Behind
+// 940 MB of writes, which the memory-side cache has yet to write back, the same
+// norm takes 140 us.  That is the clip's first pass where clips follow each
+// other: 235 M bf16 values to fp32 take 112-148 + 252 us (5.6 TB/s in the second
+// pass), 235 M fp32 values in place 531 in all.  The clip of 17 M fp32 values (67
+// MB, the second read from the memory-side cache) takes 13 + 25 us.  Four vectors
+// of 1024 values: 5 us in one workgroup, launch latency and two dependent loads.
 #include <type_traits>
 
 #include "inputs.h"
