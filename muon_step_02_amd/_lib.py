@@ -494,7 +494,8 @@ def _rows_of(t):
 
 def muon_grad(grad, out=None):
     """Descriptor of one gradient for :func:`muon_grad_norm` and, with ``out``
-    (the gradient itself clips in place), :func:`muon_grad_clip`."""
+    (the gradient itself clips in place), :func:`muon_grad_clip`.  It keeps both
+    tensors alive."""
     if out is not None and out.device != grad.device:
         raise ValueError("the gradient is on %s, its output on %s" % (grad.device, out.device))
     rows, cols, ld = _rows_of(grad)

@@ -389,3 +389,16 @@ def test_large_products_at_other_alignments_read_no_other_group():
         assert torch.equal(got[:3001], want[:3001]) and torch.equal(got[7098:], want[7098:])
     for e in (0, 2):
         assert torch.equal(a.dw[e], b.dw[e])
+
+
+# Above 128 experts the kernels take longer lists of pointers, as variants of their
+# own: 32 x 64, 128 x 128 and 256 x 256 tiles (by the rows of a group), tiles
+# through registers of both sizes, and fp32.
+@pytest.mark.parametrize("mean,rows,cols,dtype,grad_dtype", [
+    (4, 256, 264, BF16, F32), (40, 264, 256, BF16, BF16), (200, 256, 256, BF16, F32), (20, 65, 63, BF16, BF16),
+    (40, 1301, 383, BF16, F32), (20, 72, 100, F32, F32)],
+    ids=["few rows", "128 x 128", "256 x 256", "registers", "registers, 128 x 128", "fp32"])
+def test_more_than_128_experts(mean, rows, cols, dtype, grad_dtype):
+    r = torch.Generator().manual_seed(mean)
+    sizes = (torch.rand(130, generator=r) * 2 * mean).int().tolist()
+    Layer(sizes, rows, cols, dtype, grad_dtype=grad_dtype, seed=rows).check()

@@ -270,3 +270,22 @@ def test_the_workspace_is_as_large_as_its_size_says(shapes):
     mu.muon_grad_norm(h, plan, 1.0, buf[:need], norm_out=norm)
     _check_norm(norm, _reference(grads, 1.0)[0])
     assert bool((buf[need:] == 0xA5).all())
+
+
+def test_both_types_in_one_call():
+    """fp32 and bf16 gradients, outputs of either type and in place."""
+    h = Handle.get()
+    F32, BF16 = torch.float32, torch.bfloat16
+    shapes = SETS["odd rows"] + SETS["vectors"] + SETS["several chunks"]
+    grads, outs = [], []
+    for i, s in enumerate(shapes):
+        grads += _make([s], (F32, BF16)[i % 2], i)[0]
+        outs += _make([s], (F32, BF16)[i // 2 % 2], 100 + i)[0]
+    outs = [g if i % 5 == 0 else o for i, (g, o) in enumerate(zip(grads, outs))]
+    before = [g.clone() for g in grads]
+    norm, _ = _reference(before, 1.0)
+    plan = [mu.muon_grad(g, o) for g, o in zip(grads, outs)]
+    got = torch.zeros(1, device=DEV)
+    mu.muon_grad_clip(h, plan, 0.3 * norm, _workspace(h, plan), norm_out=got)
+    _check_norm(got, norm)
+    _check_outs(before, outs, 0.3)

@@ -332,3 +332,14 @@ def test_the_workspace_is_as_large_as_its_size_says(nq, nk, dtype, dim):
     mu.muon_qk_smax(h, q, k, cu_q, cu_k, sq, buf[:need], scale=1.0)
     assert torch.equal(sq, _reference(q, k, at_q, at_k, 1.0, True)[0].float())
     assert bool((buf[need:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("sequences", [64, 65, 200])
+def test_many_sequences(sequences, dtype):
+    """More than a wave's lanes, some empty, a few of them long."""
+    r = torch.Generator().manual_seed(sequences)
+    nq = (torch.rand(sequences, generator=r) * 20 - 2).clamp(min=0).int().tolist()
+    nq[3], nq[-2] = 300, 170
+    nk = [n + i % 3 for i, n in enumerate(nq)]
+    _check_whole(_ints(33, sum(nq), 4, 64, dtype), _ints(34, sum(nk), 2, 64, dtype), nq, nk, True)
