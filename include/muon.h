@@ -407,6 +407,183 @@ muon_status muon_qk_smax_workspace_size(muon_handle h, const muon_qk* qk, size_t
 muon_status muon_qk_smax(muon_handle h, const muon_qk* qk, float* smax_q, float* smax_k,
                          int accumulate, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- around the products and the logits -------------------------------------
+ * Operators that make what the calls above read and that carry gradients back
+ * through them: layer norm (in front of a projection, or of every head of q and
+ * k), rotary positions on q and k, and the router of a mixture-of-experts layer,
+ * whose offsets the experts' products take.  The rules are the same: caller-owned
+ * device memory, validation before anything is enqueued, work on `stream` only,
+ * no wait on the host, capture allowed.  Positions, choices and counts are
+ * device data that the host never reads. */
+
+/* Values of one tensor: element d of head h of token t at
+ * data[t * token + h * head + d] (strides in elements, >= 0).  A matrix is one
+ * head a token.  What a call writes needs heads or tokens that lie one behind
+ * the other without sharing elements: token >= (heads - 1) * head + width and
+ * head >= width, or the same with tokens and heads exchanged. */
+typedef struct {
+    void* data;
+    int64_t token, head;
+    int32_t heads;
+} muon_heads;
+
+/* Layer norm over the last dimension of `tokens` x heads rows of cols values
+ * (cols <= 16384), F32 or BF16:
+ *   mean = sum x / cols with center, else 0 (root mean square norm)
+ *   rstd = 1 / sqrt(sum (x - mean)^2 / cols + eps)
+ *   xhat = (x - mean) * rstd,   y = xhat * weight + bias
+ * weight, bias: cols values of weight_dtype; NULL: ones, zeros. */
+typedef struct {
+    const void* weight;
+    const void* bias; /* forward only */
+    int64_t tokens, cols;
+    int32_t dtype;        /* muon_dtype of the rows */
+    int32_t weight_dtype; /* muon_dtype */
+    int32_t center;       /* 0 or 1 */
+    float eps;            /* >= 0; forward only */
+} muon_layernorm;
+
+/* y from x; mean and rstd (tokens * heads floats, by token, then head) are
+ * written where they are not NULL.  Statistics are fp32 sums over a row held in
+ * registers, the variance that of the differences from the mean; y is rounded
+ * once.  y may be x itself (the same strides).  Rejects sizes or strides out of
+ * range, null or misaligned pointers, and outputs that share memory with
+ * anything else of the call (MUON_ERR_OVERLAP; strided ranges that cannot be
+ * told apart count as shared). */
+muon_status muon_layernorm_forward(muon_handle h, const muon_layernorm* n, const muon_heads* x,
+                                   const muon_heads* y, float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace for muon_layernorm_grad of `heads` heads a token (sizes
+ * and types matter, pointers do not). */
+muon_status muon_layernorm_workspace_size(muon_handle h, const muon_layernorm* n, int32_t heads,
+                                          size_t* bytes);
+
+/* The gradient, with g = dy * weight and the forward pass's mean (with center)
+ * and rstd:
+ *   dx = rstd * (g - xhat * sum(g * xhat) / cols - [center] sum g / cols)
+ *   dweight = sum over rows of dy * xhat,   dbias = sum over rows of dy
+ * Each of dx, dweight and dbias may be NULL (not wanted; one of them at least).
+ * dx may be x or dy itself.  dweight and dbias: cols values of grad_dtype, added
+ * to what they hold with accumulate; rows are summed in fp32 by workgroup, then
+ * in 64 bits, in a fixed order: results are bitwise repeatable.  Without rows
+ * they are zero, or left as they are with accumulate.
+ * workspace: muon_layernorm_workspace_size bytes, 256-byte aligned, not shared
+ * by calls that may overlap in time.  Rejects as the forward pass does. */
+muon_status muon_layernorm_grad(muon_handle h, const muon_layernorm* n, const muon_heads* x,
+                                const muon_heads* dy, const float* mean, const float* rstd,
+                                const muon_heads* dx, void* dweight, void* dbias, int32_t grad_dtype,
+                                int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Frequencies of a head's pairs, in radians a position, into out[pairs] (HOST
+ * doubles; the caller copies them to the device once):
+ *   NONE    f_i = base^(-i / pairs)
+ *   LINEAR  f_i / factor
+ *   BASE    NONE with base * factor^(pairs / (pairs - 1)): f_0 stays, the last
+ *           one falls by factor (pairs >= 2)
+ *   PARTS   f_i * (k + (1 - k) / factor), k = (context * f_i / (2 pi) - low) /
+ *           (high - low) within [0, 1]: pairs that make more than `high` turns
+ *           over the trained context keep their frequency, those with fewer
+ *           than `low` are interpolated (context > 0, low < high)
+ * base > 0, factor > 0, finite. */
+typedef enum {
+    MUON_ROTARY_NONE = 0,
+    MUON_ROTARY_LINEAR = 1,
+    MUON_ROTARY_BASE = 2,
+    MUON_ROTARY_PARTS = 3
+} muon_rotary_scaling;
+typedef struct {
+    int32_t scaling; /* muon_rotary_scaling */
+    int32_t pairs;
+    double base; /* typically 10000 */
+    double factor, context, low, high;
+} muon_rotary_plan;
+muon_status muon_rotary_frequencies(const muon_rotary_plan* plan, double* out);
+
+/* Rotary positions.  Elements first ... first + 2 * pairs - 1 of a head turn in
+ * pairs: (first + i, first + pairs + i), or (first + 2i, first + 2i + 1) with
+ * interleaved.  Pair i of token t turns by a = positions[t] * frequencies[i]:
+ *   (u, v) -> scale * (u cos a - v sin a, v cos a + u sin a)
+ * With transpose it turns back, by -a: dx from dy.  Other elements are copied.
+ * Angles are formed in 64 bits, products in fp32, rounded once. */
+typedef struct {
+    const int32_t* positions;  /* device, one per token, any value */
+    const double* frequencies; /* device, pairs values */
+    int64_t tokens;
+    int32_t head_dim, first, pairs; /* pairs in [1, 2048] */
+    int32_t interleaved;            /* 0 or 1 */
+    int32_t dtype;                  /* muon_dtype of every tensor */
+    float scale;                    /* finite, typically 1 */
+} muon_positions;
+
+/* Turns n tensors (1 to 4, for example q and k) in one launch: y[i] from x[i],
+ * which have equal heads; y[i] may be x[i] itself (the same strides).  Rejects
+ * sizes or strides out of range, null or misaligned pointers, and outputs that
+ * share memory with anything else of the call (MUON_ERR_OVERLAP; strided ranges
+ * that cannot be told apart count as shared). */
+muon_status muon_rotary(muon_handle h, const muon_positions* p, const muon_heads* x,
+                        const muon_heads* y, int n, int transpose, void* stream);
+
+/* Router logits, tokens (at most 2^28) x experts (at most 1024) row-major with leading
+ * dimension ld, F32 or BF16; top_k in [1, min(32, experts)].  An expert whose
+ * logit is -inf is out of reach of that token; a token whose logits are all -inf
+ * (padding) has no choices, zero probabilities and no part in the losses. */
+typedef struct {
+    const void* logits;
+    int64_t tokens, ld;
+    int32_t experts, top_k;
+    int32_t dtype;       /* muon_dtype */
+    int32_t renormalize; /* 1: a token's gates are divided by their sum */
+} muon_router;
+
+/* What the router decides (device memory; ... = may be NULL: not wanted):
+ *   chosen    tokens x top_k: the experts of the largest logits in descending
+ *             order, the lowest index first among equals; -1 where none is left
+ *   gates     tokens x top_k: softmax of the logits over all experts, at the
+ *             chosen ones; 0 where none is left
+ *   counts    experts: choices per expert
+ *   offsets   experts + 1: the prefix sums of counts, which the experts'
+ *             products take
+ *   rows ...  tokens x top_k: the choice's row in the groups, by expert, then
+ *             token; -1 where none is left
+ *   order ... tokens * top_k: the inverse, token * top_k + choice of each row;
+ *             -1 behind the last row
+ *   live ...  1: n, the tokens with a logit above -inf
+ *   losses ... 2: balance = experts * sum_e (counts_e / sum counts) *
+ *             (sum over tokens of p_e / n), and z = sum over tokens of
+ *             (log sum exp of the logits)^2 / n; zeros without tokens
+ * A NaN logit is never chosen; it makes its token's gates and the losses NaN. */
+typedef struct {
+    int32_t* chosen;
+    float* gates;
+    int32_t* counts;
+    int32_t* offsets;
+    int32_t* rows;
+    int32_t* order;
+    int32_t* live;
+    float* losses;
+} muon_routing;
+
+/* workspace: muon_router_workspace_size bytes (sizes matter, pointers do not),
+ * 256-byte aligned, not shared by calls that may overlap in time.  Probabilities
+ * are summed in fp32 over 64 tokens, then in 64 bits, in a fixed order: results
+ * are bitwise repeatable.  Rejects sizes out of range, null or misaligned
+ * pointers, a small or null workspace, and outputs or a workspace that share
+ * memory with anything else of the call (MUON_ERR_OVERLAP). */
+muon_status muon_router_workspace_size(muon_handle h, const muon_router* r, size_t* bytes);
+muon_status muon_router_forward(muon_handle h, const muon_router* r, const muon_routing* out,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* dlogits (the logits' type, leading dimension ld_dlogits) of
+ *   sum over choices of dgates * gates + balance * balance loss + z * z loss
+ * with chosen, counts and live as muon_router_forward gave them (a choice outside
+ * [0, experts) is none; one that is listed twice counts twice).  Counts are
+ * constants: the balance loss reaches the logits through the probabilities
+ * alone.  dgates (tokens x top_k) may be NULL: zeros.  Rejects as the forward
+ * pass does, and balance or z that are not finite. */
+muon_status muon_router_grad(muon_handle h, const muon_router* r, const int32_t* chosen,
+                             const int32_t* counts, const int32_t* live, const float* dgates,
+                             float balance, float z, void* dlogits, int64_t ld_dlogits, void* stream);
+
 /* Static, human readable name of a status. */
 const char* muon_status_str(muon_status s);
 

@@ -15,6 +15,9 @@ Names follow the C ABI in ``include/muon.h``:
 * :func:`muon_expert_forward`, :func:`muon_expert_grad_input`,
   :func:`muon_expert_grad_weight`
 * :func:`muon_qk_smax`
+* :func:`muon_layernorm_forward`, :func:`muon_layernorm_grad`
+* :func:`muon_rotary`, :func:`muon_rotary_frequencies`
+* :func:`muon_router_forward`, :func:`muon_router_grad`
 
 plus helpers that build the C descriptors from PyTorch tensors
 (:func:`muon_matrix`, :func:`muon_hparams`, :func:`adamw_tensor`,
@@ -29,7 +32,13 @@ from ._lib import (  # noqa: F401
     MuonError,
     MuonExperts,
     MuonGrad,
+    MuonHeads,
+    MuonLayernorm,
+    MuonPositions,
     MuonQk,
+    MuonRotaryPlan,
+    MuonRouter,
+    MuonRouting,
     AdamwHparams,
     AdamwTensor,
     MuonHparams,
@@ -54,6 +63,9 @@ from ._lib import (  # noqa: F401
     muon_grad_workspace_size,
     muon_hparams,
     muon_init,
+    muon_layernorm_forward,
+    muon_layernorm_grad,
+    muon_layernorm_workspace_size,
     muon_matrix,
     muon_profile_collect,
     muon_profile_enable,
@@ -61,6 +73,11 @@ from ._lib import (  # noqa: F401
     PHASES,
     muon_qk_smax,
     muon_qk_smax_workspace_size,
+    muon_rotary,
+    muon_rotary_frequencies,
+    muon_router_forward,
+    muon_router_grad,
+    muon_router_workspace_size,
     muon_step_batched,
     muon_step_batched_scaled,
     muon_test_gram_bf16,

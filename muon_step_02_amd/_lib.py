@@ -8,6 +8,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmuon.so"
 MUON_F32 = 0
 MUON_BF16 = 1
 SCALE_MODES = {"moonlight": 0, "jordan": 1, "bernstein": 2, "none": 3}
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
 
 STATUS = {
     0: "MUON_OK",
@@ -47,6 +48,14 @@ SYMBOLS = (
     "muon_expert_grad_weight",
     "muon_qk_smax_workspace_size",
     "muon_qk_smax",
+    "muon_layernorm_forward",
+    "muon_layernorm_workspace_size",
+    "muon_layernorm_grad",
+    "muon_rotary_frequencies",
+    "muon_rotary",
+    "muon_router_workspace_size",
+    "muon_router_forward",
+    "muon_router_grad",
 )
 
 NUM_PHASES = 7
@@ -168,6 +177,79 @@ class MuonQk(ctypes.Structure):
     ]
 
 
+class MuonHeads(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("token", ctypes.c_int64),
+        ("head", ctypes.c_int64),
+        ("heads", ctypes.c_int32),
+    ]
+
+
+class MuonLayernorm(ctypes.Structure):
+    _fields_ = [
+        ("weight", ctypes.c_void_p),
+        ("bias", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("weight_dtype", ctypes.c_int32),
+        ("center", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class MuonRotaryPlan(ctypes.Structure):
+    _fields_ = [
+        ("scaling", ctypes.c_int32),
+        ("pairs", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("context", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+    ]
+
+
+class MuonPositions(ctypes.Structure):
+    _fields_ = [
+        ("positions", ctypes.c_void_p),
+        ("frequencies", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("head_dim", ctypes.c_int32),
+        ("first", ctypes.c_int32),
+        ("pairs", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class MuonRouter(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("experts", ctypes.c_int32),
+        ("top_k", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+    ]
+
+
+class MuonRouting(ctypes.Structure):
+    _fields_ = [
+        ("chosen", ctypes.c_void_p),
+        ("gates", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("offsets", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("order", ctypes.c_void_p),
+        ("live", ctypes.c_void_p),
+        ("losses", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -217,6 +299,16 @@ def load():
                                             i64, ctypes.c_int32, i32, vp]
     lib.muon_qk_smax_workspace_size.argtypes = [vp, ctypes.POINTER(MuonQk), ctypes.POINTER(sz)]
     lib.muon_qk_smax.argtypes = [vp, ctypes.POINTER(MuonQk), vp, vp, i32, vp, sz, vp]
+    heads, norm = ctypes.POINTER(MuonHeads), ctypes.POINTER(MuonLayernorm)
+    lib.muon_layernorm_forward.argtypes = [vp, norm, heads, heads, vp, vp, vp]
+    lib.muon_layernorm_workspace_size.argtypes = [vp, norm, ctypes.c_int32, ctypes.POINTER(sz)]
+    lib.muon_layernorm_grad.argtypes = [vp, norm, heads, heads, vp, vp, heads, vp, vp, ctypes.c_int32, i32,
+                                        vp, sz, vp]
+    lib.muon_rotary_frequencies.argtypes = [ctypes.POINTER(MuonRotaryPlan), ctypes.POINTER(ctypes.c_double)]
+    lib.muon_rotary.argtypes = [vp, ctypes.POINTER(MuonPositions), heads, heads, i32, i32, vp]
+    lib.muon_router_workspace_size.argtypes = [vp, ctypes.POINTER(MuonRouter), ctypes.POINTER(sz)]
+    lib.muon_router_forward.argtypes = [vp, ctypes.POINTER(MuonRouter), ctypes.POINTER(MuonRouting), vp, sz, vp]
+    lib.muon_router_grad.argtypes = [vp, ctypes.POINTER(MuonRouter), vp, vp, vp, vp, f32, f32, vp, i64, vp]
     lib.muon_profile_enable.argtypes = [vp, i32]
     lib.muon_profile_collect.argtypes = [vp, ctypes.POINTER(PhaseTimes)]
     for name in ("muon_init", "muon_destroy", "muon_workspace_size", "muon_step_batched",
@@ -226,7 +318,9 @@ def load():
                  "adamw_step_clipped_noalloc", "muon_step_batched_scaled", "adamw_step_scaled",
                  "muon_grad_workspace_size", "muon_grad_norm", "muon_grad_clip",
                  "muon_expert_forward", "muon_expert_grad_input", "muon_expert_grad_weight",
-                 "muon_qk_smax_workspace_size", "muon_qk_smax"):
+                 "muon_qk_smax_workspace_size", "muon_qk_smax", "muon_layernorm_forward",
+                 "muon_layernorm_workspace_size", "muon_layernorm_grad", "muon_rotary_frequencies",
+                 "muon_rotary", "muon_router_workspace_size", "muon_router_forward", "muon_router_grad"):
         getattr(lib, name).restype = i32
     _lib = lib
     return lib
@@ -669,6 +763,205 @@ def muon_qk_smax(h, q, k, cu_q, cu_k, smax_q, workspace, smax_k=None, scale=None
                                smax_k.data_ptr() if smax_k is not None else None,
                                1 if accumulate else 0, workspace.data_ptr(), _nbytes(workspace),
                                _stream_on(stream, dev, h)), "muon_qk_smax")
+
+
+def _heads(t, what):
+    """Descriptor of a (tokens, heads, width) tensor, or of a (tokens, width)
+    one as one head a token."""
+    n = t.dim()
+    if n == 3:
+        tokens, heads, width = t.shape
+        s, sh, sw = t.stride()
+    elif n == 2:
+        (tokens, width), heads = t.shape, 1
+        (s, sw), sh = t.stride(), width
+    else:
+        raise ValueError("%s must be (tokens, heads, width) or (tokens, width)" % what)
+    if sw != 1 and width > 1:
+        raise ValueError("%s needs unit stride in its last dimension" % what)
+    # the stride of a dimension of one element says nothing
+    if heads == 1:
+        sh = width
+    if tokens <= 1:
+        s = heads * sh
+    return MuonHeads(t.data_ptr(), s, sh, heads)
+
+
+def _vector(t, numel, dtype, what):
+    """Pointer of a contiguous tensor of `numel` values (None: not given)."""
+    if t is None:
+        return None
+    if t.numel() != numel or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        raise ValueError("%s must be contiguous, %d values%s" % (what, numel, "" if dtype is None else " of %s" % dtype))
+    return t.data_ptr()
+
+
+def _layernorm(x, weight, bias, center, eps):
+    cols = x.shape[-1]
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias differ in type")
+    w = weight if weight is not None else bias
+    return MuonLayernorm(_vector(weight, cols, None, "weight"), _vector(bias, cols, None, "bias"), x.shape[0], cols,
+                         _dt(x), _dt(w) if w is not None else MUON_F32, 1 if center else 0, eps)
+
+
+def muon_layernorm_forward(h, x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5, center=True,
+                           stream=None):
+    """Layer norm over the last dimension of ``x`` (tokens, width) or (tokens,
+    heads, width), any strides but the last: ``y`` = (x - mean) * rstd * weight +
+    bias; ``y`` may be ``x`` itself.  ``mean`` and ``rstd`` (float32, one value per
+    row; optional) receive the statistics that :func:`muon_layernorm_grad` reads.
+    Without ``center`` the mean is taken as zero (root mean square norm)."""
+    import torch
+    dev = _same_device(x, y, weight, bias, mean, rstd)
+    if y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError("x and y differ in shape or type")
+    n, hx, hy = _layernorm(x, weight, bias, center, eps), _heads(x, "x"), _heads(y, "y")
+    rows = x.shape[0] * hx.heads
+    _check(load().muon_layernorm_forward(h, n, hx, hy, _vector(mean, rows, torch.float32, "mean"),
+                                         _vector(rstd, rows, torch.float32, "rstd"), _stream_on(stream, dev, h)),
+           "muon_layernorm_forward")
+
+
+def muon_layernorm_workspace_size(h, x):
+    """Workspace bytes of :func:`muon_layernorm_grad` for an ``x`` of this shape and type."""
+    sz = ctypes.c_size_t()
+    n = _layernorm(x, None, None, True, 0.0)
+    _check(load().muon_layernorm_workspace_size(h, n, _heads(x, "x").heads, sz), "muon_layernorm_workspace_size")
+    return sz.value
+
+
+def muon_layernorm_grad(h, x, dy, rstd, workspace, mean=None, weight=None, dx=None, dweight=None, dbias=None,
+                        accumulate=False, center=True, stream=None):
+    """Gradients of :func:`muon_layernorm_forward` from its ``mean`` (with
+    ``center``) and ``rstd``: ``dx`` (which may be ``x`` or ``dy`` itself), and
+    ``dweight`` and ``dbias`` of one type, added to what they hold with
+    ``accumulate``.  Each is optional."""
+    import torch
+    dev = _same_device(x, dy, rstd, workspace, mean, weight, dx, dweight, dbias)
+    for t in (dy, dx):
+        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+            raise ValueError("x, dy and dx differ in shape or type")
+    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
+        raise TypeError("dweight and dbias differ in type")
+    n, hx, hdy = _layernorm(x, weight, None, center, 0.0), _heads(x, "x"), _heads(dy, "dy")
+    rows, cols = x.shape[0] * hx.heads, x.shape[-1]
+    if center and mean is None:
+        raise ValueError("a centered norm needs its mean")
+    g = dweight if dweight is not None else dbias
+    _check(load().muon_layernorm_grad(
+        h, n, hx, hdy, _vector(mean, rows, torch.float32, "mean"), _vector(rstd, rows, torch.float32, "rstd"),
+        _heads(dx, "dx") if dx is not None else None, _vector(dweight, cols, None, "dweight"),
+        _vector(dbias, cols, None, "dbias"), _dt(g) if g is not None else MUON_F32, 1 if accumulate else 0,
+        workspace.data_ptr(), _nbytes(workspace), _stream_on(stream, dev, h)), "muon_layernorm_grad")
+
+
+def muon_rotary_frequencies(pairs, base=10000.0, scaling="none", factor=1.0, context=0.0, low=1.0, high=32.0):
+    """Radians a position of each pair of a head (float64, on the host: copy it to
+    the device once), ``scaling`` for longer contexts: "none", "linear", "base" or
+    "parts" (``include/muon.h`` has the formulas)."""
+    import torch
+    out = (ctypes.c_double * max(int(pairs), 1))()
+    plan = MuonRotaryPlan(ROTARY_SCALINGS[scaling], pairs, base, factor, context, low, high)
+    _check(load().muon_rotary_frequencies(plan, out), "muon_rotary_frequencies")
+    return torch.tensor(list(out), dtype=torch.float64)
+
+
+def muon_rotary(h, x, y, positions, frequencies, first=0, interleaved=False, scale=1.0, transpose=False,
+                stream=None):
+    """Rotary positions: ``y`` from ``x``, a tensor (tokens, heads, head_dim) or a
+    list of up to four of them (q and k) that differ in heads at most; ``y`` may be
+    ``x`` itself.  Elements ``first`` to ``first`` + 2 * pairs - 1 of every head turn
+    by ``positions`` (int32, one per token) * ``frequencies`` (float64, one per pair:
+    :func:`muon_rotary_frequencies`), the pairs neighbours with ``interleaved``,
+    else half the turning part apart; other elements are copied.  ``transpose``
+    turns back: dx from dy."""
+    import torch
+    xs = x if isinstance(x, (list, tuple)) else (x,)
+    ys = y if isinstance(y, (list, tuple)) else (y,)
+    n = len(xs)
+    if n != len(ys) or not 1 <= n <= 4:
+        raise ValueError("expected one to four tensors and as many outputs")
+    dev = _same_device(positions, frequencies, *xs, *ys)
+    x0 = xs[0]
+    tokens, dim, dtype = x0.shape[0], x0.shape[-1], x0.dtype
+    for a, b in zip(xs, ys):
+        if a.shape != b.shape or a.shape[0] != tokens or a.shape[-1] != dim or a.dtype != dtype or b.dtype != dtype:
+            raise ValueError("the tensors differ in tokens, head size or type, or from their outputs in shape")
+    if positions.numel() != tokens:
+        raise ValueError("positions must hold one value per token")
+    pairs = frequencies.numel()
+    p = MuonPositions(_int32(positions, "positions"), _vector(frequencies, pairs, torch.float64, "frequencies"),
+                      tokens, dim, first, pairs, 1 if interleaved else 0, _dt(x0), scale)
+    hs = MuonHeads * n
+    _check(load().muon_rotary(h, p, hs(*[_heads(t, "x") for t in xs]), hs(*[_heads(t, "y") for t in ys]), n,
+                              1 if transpose else 0, _stream_on(stream, dev, h)), "muon_rotary")
+
+
+def _router(logits, top_k, renormalize):
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2D with unit column stride")
+    tokens, experts = logits.shape
+    return MuonRouter(logits.data_ptr(), tokens, logits.stride(0) if tokens > 1 else experts, experts, top_k,
+                      _dt(logits), 1 if renormalize else 0)
+
+
+def _choices(t, tokens, dtype, what):
+    """(pointer, top_k) of a contiguous (tokens, top_k) tensor."""
+    if t.dim() != 2 or t.shape[0] != tokens or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous (tokens, top_k) tensor of %s" % (what, dtype))
+    return t.data_ptr(), t.shape[1]
+
+
+def muon_router_workspace_size(h, logits, top_k):
+    """Workspace bytes of :func:`muon_router_forward` for logits of this shape."""
+    sz = ctypes.c_size_t()
+    _check(load().muon_router_workspace_size(h, _router(logits, top_k, False), sz), "muon_router_workspace_size")
+    return sz.value
+
+
+def muon_router_forward(h, logits, chosen, gates, counts, offsets, workspace, rows=None, order=None, live=None,
+                        losses=None, renormalize=False, stream=None):
+    """The router of a mixture-of-experts layer.  ``logits`` (tokens, experts);
+    ``chosen`` (int32) and ``gates`` (float32), both (tokens, top_k): the experts of
+    the largest logits and their softmax probabilities (divided by their sum with
+    ``renormalize``); ``counts`` (experts) and ``offsets`` (experts + 1, int32): what
+    :func:`muon_expert_forward` takes.  Optional: ``rows`` (tokens, top_k), each
+    choice's row in the groups, and ``order`` (tokens * top_k), its inverse, so that
+    ``x[order // top_k]`` is grouped by expert; ``live`` (1 int32), the tokens that
+    have a logit above -inf; ``losses`` (2 float32): the balance and the z loss."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    dev = _same_device(logits, chosen, gates, counts, offsets, workspace, rows, order, live, losses)
+    pc, top_k = _choices(chosen, logits.shape[0], i32, "chosen")
+    r = _router(logits, top_k, renormalize)
+    n = r.tokens * top_k
+    if gates.shape != chosen.shape or (rows is not None and rows.shape != chosen.shape):
+        raise ValueError("chosen, gates and rows differ in shape")
+    out = MuonRouting(pc, _vector(gates, n, f32, "gates"), _vector(counts, r.experts, i32, "counts"),
+                      _vector(offsets, r.experts + 1, i32, "offsets"), _vector(rows, n, i32, "rows"),
+                      _vector(order, n, i32, "order"), _vector(live, 1, i32, "live"),
+                      _vector(losses, 2, f32, "losses"))
+    _check(load().muon_router_forward(h, r, out, workspace.data_ptr(), _nbytes(workspace),
+                                      _stream_on(stream, dev, h)), "muon_router_forward")
+
+
+def muon_router_grad(h, logits, chosen, counts, live, dlogits, dgates=None, balance=0.0, z=0.0,
+                     renormalize=False, stream=None):
+    """``dlogits`` of sum(``dgates`` * gates) + ``balance`` * balance loss + ``z`` * z
+    loss, with what :func:`muon_router_forward` gave."""
+    import torch
+    dev = _same_device(logits, chosen, counts, live, dlogits, dgates)
+    pc, top_k = _choices(chosen, logits.shape[0], torch.int32, "chosen")
+    r = _router(logits, top_k, renormalize)
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or \
+            (r.experts > 1 and dlogits.stride(1) != 1):
+        raise ValueError("dlogits must have the logits' shape and type, and unit column stride")
+    _check(load().muon_router_grad(h, r, pc, _vector(counts, r.experts, torch.int32, "counts"),
+                                   _vector(live, 1, torch.int32, "live"),
+                                   _vector(dgates, r.tokens * top_k, torch.float32, "dgates"), balance, z,
+                                   dlogits.data_ptr(), dlogits.stride(0) if r.tokens > 1 else r.experts,
+                                   _stream_on(stream, dev, h)), "muon_router_grad")
 
 
 def muon_test_gram_bf16(h, X, A, m, n, ldx, lda, s2=1.0, stream=None):

@@ -16,7 +16,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libmuon.so")
 
 SOURCES = ["api.hip", "plan.cpp", "elementwise.hip", "gemm_bf16.hip", "gemm_f32.hip",
-           "api_inputs.hip", "grads.hip", "experts.hip", "qk_smax.hip"]
+           "api_inputs.hip", "grads.hip", "experts.hip", "qk_smax.hip",
+           "api_block.hip", "layernorm.hip", "rotary.hip", "router.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -21,6 +21,7 @@ namespace muon {
 // global address space makes the compiler emit global_* instructions.
 #define MUON_GLOBAL __attribute__((address_space(1)))
 template <int BYTES> struct GWord;
+template <> struct GWord<1> { using T = uint8_t; };
 template <> struct GWord<2> { using T = uint16_t; };
 template <> struct GWord<4> { using T = uint32_t; };
 template <> struct GWord<8> { using T = uint32_t __attribute__((ext_vector_type(2))); };

@@ -1,0 +1,552 @@
+// The router of a mixture-of-experts layer, and its gradient (gfx950).
+//
+//   p = softmax(z) over the experts of a token, lse = log sum exp z
+//   chosen = the k largest logits, the lowest index first among equals
+//   gates = p[chosen], or p[chosen] over their sum
+//   counts, offsets = choices per expert and their prefix sums
+//   rows = a choice's place in the order by (expert, token); order: the inverse
+//   balance = E sum_e (counts_e / sum counts) (sum_t p_te / n)
+//   z loss = sum_t lse_t^2 / n,   n = tokens with a logit above -inf
+//
+// Three launches.  A workgroup takes 64 tokens, a team of 1 to 64 lanes one of
+// them at a time, with 8 (16 beyond 512 experts) logits a lane in registers.
+// Which of the 64 tokens chose an expert is one 64-bit mask in LDS: its bits
+// count the choices, and those below a token's own are the token's place among
+// them, whatever order the bits were set in.  The second launch adds up the
+// workgroups' counts and probabilities per expert, the third gives every choice
+// its row.  At most 64 tokens go through one workgroup in one launch.
+//
+// Gradient, with g_e = B E counts_e / (sum counts n) + [e chosen] dgate:
+//
+//   dz = p (g - sum p g + 2 Z lse / n)
+//
+// where gates were divided by their sum, their part of dz is
+// gate_j (dgate_j - sum gate dgate) instead.
+#include <math.h>
+
+#include <type_traits>
+
+#include "block.h"
+#include "team.h"
+#include "units.h"
+
+namespace muon {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = kThreads / 64;
+constexpr int kNone = 0x7fffffff;
+
+// A token's logits over the L lanes of a team: lane l holds C from l * C on,
+// -inf behind the last.
+template <bool BF, int C>
+__device__ __forceinline__ void load_logits(const void* base, int64_t off, int left, float* z) {
+    constexpr int V = BF ? 8 : 4;
+#pragma unroll
+    for (int p = 0; p < C; p += V) {
+        const Raw<BF, V> r = load_raw<BF, V, false>(base, off + p, left - p);
+#pragma unroll
+        for (int e = 0; e < V; ++e) z[p + e] = p + e < left ? r.at(e) : -INFINITY;
+    }
+}
+
+struct Softmax {
+    float top, total;  // largest logit, sum of exp(z - top)
+    bool live;
+};
+
+// e = exp(z - top) in place of nothing: z stays.  A token without any logit
+// above -inf gets zeros.
+template <int L, int C>
+__device__ __forceinline__ Softmax softmax(const float* z, float* e) {
+    float m = -INFINITY, any = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        m = fmaxf(m, z[i]);
+        any = z[i] == -INFINITY ? any : 1.f;  // a NaN counts
+    }
+    m = team_reduce<L>(m, [](float a, float b) { return fmaxf(a, b); });
+    any = team_reduce<L>(any, [](float a, float b) { return fmaxf(a, b); });
+    Softmax s;
+    s.live = any > 0.f;
+    s.top = m;
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        e[i] = s.live ? expf(z[i] - m) : 0.f;
+        t += e[i];
+    }
+    s.total = team_sum<L>(t);
+    return s;
+}
+
+// The largest of the team's logits and its index, the lowest among equals;
+// kNone where none is above -inf.
+template <int HALF>
+__device__ __forceinline__ void best_step(float& v, int& i) {
+    float ov;
+    int oi;
+    if constexpr (HALF >= 16) {
+        // each lane of a half sees the other half's pair: the two outputs hold
+        // both halves in every lane, and the better one of the two is the same
+        const uint32_t b = __builtin_bit_cast(uint32_t, v);
+        const auto s = HALF == 16 ? __builtin_amdgcn_permlane16_swap(b, b, false, false)
+                                  : __builtin_amdgcn_permlane32_swap(b, b, false, false);
+        const auto t = HALF == 16 ? __builtin_amdgcn_permlane16_swap((uint32_t)i, (uint32_t)i, false, false)
+                                  : __builtin_amdgcn_permlane32_swap((uint32_t)i, (uint32_t)i, false, false);
+        v = __builtin_bit_cast(float, (uint32_t)s[0]);
+        i = (int)t[0];
+        ov = __builtin_bit_cast(float, (uint32_t)s[1]);
+        oi = (int)t[1];
+    } else {
+        constexpr int ctrl = HALF == 1 ? 0xb1 : HALF == 2 ? 0x4e : HALF == 4 ? 0x141 : 0x140;
+        ov = __builtin_bit_cast(float, lane_move<ctrl>(__builtin_bit_cast(uint32_t, v)));
+        oi = (int)lane_move<ctrl>((uint32_t)i);
+    }
+    if (ov > v || (ov == v && oi < i)) {
+        v = ov;
+        i = oi;
+    }
+}
+
+template <int L, int C>
+__device__ __forceinline__ void best(const float* z, int first, float& v, int& i) {
+    v = -INFINITY;
+    i = kNone;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (z[c] > v) {
+            v = z[c];
+            i = first + c;
+        }
+    if constexpr (L > 1) best_step<1>(v, i);
+    if constexpr (L > 2) best_step<2>(v, i);
+    if constexpr (L > 4) best_step<4>(v, i);
+    if constexpr (L > 8) best_step<8>(v, i);
+    if constexpr (L > 16) best_step<16>(v, i);
+    if constexpr (L > 32) best_step<32>(v, i);
+}
+
+// The exclusive prefix sums of n <= 1024 counts, and their sum at [n].
+__device__ __forceinline__ void prefix_counts(int32_t* s, int n, int32_t* wave_sum) {
+    constexpr int Q = kRouterMaxExperts / kThreads;
+    int v[Q], sum = 0;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int i = threadIdx.x * Q + q;
+        v[q] = i < n ? s[i] : 0;
+        sum += v[q];
+    }
+    int upto = sum;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int up = __shfl_up(upto, off, 64);
+        if ((threadIdx.x & 63) >= off) upto += up;
+    }
+    if ((threadIdx.x & 63) == 63) wave_sum[threadIdx.x >> 6] = upto;
+    __syncthreads();  // every count is read, every wave's sum is there
+    int at = upto - sum;
+    for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) at += wave_sum[w];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        const int i = threadIdx.x * Q + q;
+        if (i < n) s[i] = at;
+        at += v[q];
+    }
+    if (threadIdx.x == kThreads - 1) s[n] = at;
+    __syncthreads();
+}
+
+// Both losses, by one workgroup: thread t's terms, added over the workgroup.
+__device__ __forceinline__ double add_up(double v, double* red) {
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double s = red[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) s += red[w];
+    return s;
+}
+
+// The rows of one workgroup's choices: `first` + the place among the masks'
+// tokens.  order behind the last row is -1.
+__device__ __forceinline__ void put_rows(const RouterCall& c, const unsigned long long* mask, const int32_t* first,
+                                         int32_t all, int token0, int tokens, const int32_t* chosen) {
+    for (int i = threadIdx.x; i < tokens * c.top_k; i += kThreads) {
+        const int e = chosen[i], t = (uint32_t)i / (uint32_t)c.top_k;
+        const int64_t at = (int64_t)token0 * c.top_k + i;
+        int row = -1;
+        if (e >= 0) row = first[e] + __popcll(mask[e] & ((1ull << t) - 1));
+        if (c.rows) gst(c.rows + at, row);
+        if (c.order) {
+            if (row >= 0) gst(c.order + row, (int32_t)at);
+            if (at >= all) gst(c.order + at, -1);
+        }
+    }
+}
+
+// Dynamic LDS of the two kernels over tokens, in this order; every part is a
+// multiple of 8 bytes.
+struct RouterLds {
+    unsigned long long* mask;  // [experts]
+    int32_t* first;            // [experts + 1]
+    float* probs;              // [waves][experts]
+    int32_t* chosen;           // [64 * top_k]
+    float* gates;              // [64 * top_k]
+    __device__ __forceinline__ RouterLds(char* p, int experts, int top_k) {
+        const int even = (experts + 1) & ~1;
+        mask = reinterpret_cast<unsigned long long*>(p);
+        first = reinterpret_cast<int32_t*>(mask + experts);
+        probs = reinterpret_cast<float*>(first + even + 2);
+        chosen = reinterpret_cast<int32_t*>(probs + kWaves * even);
+        gates = reinterpret_cast<float*>(chosen + kRouterTokens * top_k);
+    }
+};
+size_t router_lds(int experts, int top_k) {
+    const size_t even = ((size_t)experts + 1) & ~(size_t)1;
+    return (size_t)experts * 8 + (even + 2) * 4 + kWaves * even * 4 + (size_t)kRouterTokens * top_k * 8;
+}
+
+__device__ __forceinline__ void put_losses(const RouterCall& c, double balance, int64_t choices, double lse2,
+                                           int32_t live) {
+    if (c.live) gst(c.live, live);
+    if (!c.losses) return;
+    const double n = live > 0 ? live : 1;
+    gst(c.losses, (float)(choices > 0 ? c.experts * (balance / (double)choices) / n : 0.0 * balance));
+    gst(c.losses + 1, (float)(lse2 / n));
+}
+
+// Softmax, choices, gates, and the workgroup's sums.  ONE: the workgroup has
+// every token, and does the rest too.
+template <bool BF, int L, int C, bool ONE>
+__global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, RouterSpace s) {
+    extern __shared__ __align__(16) char lds[];
+    __shared__ double red[kWaves];
+    __shared__ int32_t wave_sum[kWaves];
+    constexpr int TEAMS = 64 / L;  // of a wave
+    const RouterLds m(lds, c.experts, c.top_k);
+    const int lane = threadIdx.x & 63, l = lane % L, team = lane / L, wave = threadIdx.x >> 6;
+    const int token0 = blockIdx.x * kRouterTokens, tokens = min(kRouterTokens, c.tokens - token0);
+    for (int e = threadIdx.x; e < c.experts; e += kThreads) m.mask[e] = 0;
+    __syncthreads();
+
+    float probs[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) probs[i] = 0.f;
+    double lse2 = 0.0;
+    int live = 0;
+    for (int first = wave * TEAMS; first < tokens; first += kWaves * TEAMS) {
+        const int t = first + team;
+        const bool has = t < tokens;
+        float z[C], e[C];
+        load_logits<BF, C>(c.logits, (int64_t)(token0 + (has ? t : 0)) * c.ld + l * C, has ? c.experts - l * C : 0, z);
+        const Softmax x = softmax<L, C>(z, e);
+        const float inv = x.live ? 1.f / x.total : 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) probs[i] = fmaf(e[i], inv, probs[i]);
+        if (l == 0 && x.live) {
+            const double lse = (double)x.top + (double)logf(x.total);
+            lse2 = fma(lse, lse, lse2);
+            ++live;
+        }
+        // one choice after the other
+        float sum = 0.f;
+        for (int j = 0; j < c.top_k; ++j) {
+            float v;
+            int i;
+            best<L, C>(z, l * C, v, i);
+            const bool some = i != kNone;
+#pragma unroll
+            for (int k = 0; k < C; ++k)
+                if (l * C + k == i) z[k] = -INFINITY;
+            const float g = some ? expf(v - x.top) : 0.f;
+            sum += g;
+            if (l == 0 && has) {
+                m.chosen[t * c.top_k + j] = some ? i : -1;
+                m.gates[t * c.top_k + j] = g;
+                if (some) atomicOr(m.mask + i, 1ull << t);
+            }
+        }
+        // a NaN logit, which x.total has seen, makes its token's gates NaN
+        float by = c.renormalize ? fmaf(0.f, x.total, sum) : x.total;
+        if (by == 0.f) by = 1.f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        if (has)
+            for (int j = l; j < c.top_k; j += L) m.gates[t * c.top_k + j] /= by;
+    }
+    // the teams of a wave have the same experts in the same lanes
+#pragma unroll
+    for (int off = L; off < 64; off <<= 1)
+#pragma unroll
+        for (int i = 0; i < C; ++i) probs[i] += __shfl_xor(probs[i], off, 64);
+    const int even = (c.experts + 1) & ~1;
+    if (team == 0)
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+            if (l * C + i < c.experts) m.probs[wave * even + l * C + i] = probs[i];
+    lse2 = add_up(lse2, red);
+    const int32_t alive = (int32_t)add_up((double)live, red);  // (both pass barriers: LDS is whole)
+
+    const int64_t at = (int64_t)token0 * c.top_k;
+    for (int i = threadIdx.x; i < tokens * c.top_k; i += kThreads) {
+        gst(c.chosen + at + i, m.chosen[i]);
+        gst(c.gates + at + i, m.gates[i]);
+    }
+    double balance = 0.0;
+    for (int e = threadIdx.x; e < c.experts; e += kThreads) {
+        const int n = __popcll(m.mask[e]);
+        float p = m.probs[e];
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) p += m.probs[w * even + e];
+        if (ONE) {
+            m.first[e] = n;
+            gst(c.counts + e, n);
+            balance = fma((double)n, (double)p, balance);
+        } else {
+            gst(s.hist + (int64_t)blockIdx.x * c.experts + e, (uint8_t)n);
+            gst(s.probs + (int64_t)blockIdx.x * c.experts + e, p);
+        }
+    }
+    if (!ONE) {
+        if (threadIdx.x == 0) {
+            gst(s.lse + blockIdx.x, lse2);
+            gst(s.live + blockIdx.x, alive);
+        }
+        return;
+    }
+    balance = add_up(balance, red);  // (and every count is in LDS)
+    prefix_counts(m.first, c.experts, wave_sum);
+    const int32_t all = m.first[c.experts];
+    for (int e = threadIdx.x; e <= c.experts; e += kThreads) gst(c.offsets + e, m.first[e]);
+    if (c.rows || c.order) put_rows(c, m.mask, m.first, all, token0, tokens, m.chosen);
+    if (threadIdx.x == 0) put_losses(c, balance, all, lse2, alive);
+}
+
+// Per expert: the workgroups' choices before each workgroup, and the sums over
+// all of them.  16 experts a workgroup; 64 threads an expert, each a run of
+// workgroups.
+constexpr int kJoinExperts = 16;
+
+__global__ __launch_bounds__(1024) void router_join_kernel(RouterCall c, RouterSpace s) {
+    __shared__ int32_t count[kJoinExperts][64];
+    __shared__ double prob[kJoinExperts][64];
+    const int x = threadIdx.x % kJoinExperts, run = threadIdx.x / kJoinExperts;
+    const int e = blockIdx.x * kJoinExperts + x, each = (s.blocks + 63) / 64;
+    const int b0 = min(run * each, s.blocks), b1 = min(b0 + each, s.blocks);
+    int n = 0;
+    double p = 0.0;
+    if (e < c.experts)
+        for (int b = b0; b < b1; ++b) {
+            n += gld(s.hist + (int64_t)b * c.experts + e);
+            p += gld(s.probs + (int64_t)b * c.experts + e);
+        }
+    count[x][run] = n;
+    prob[x][run] = p;
+    __syncthreads();
+    {  // a wave an expert
+        const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, mine = blockIdx.x * kJoinExperts + w;
+        const int own = count[w][lane];
+        int upto = own;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int up = __shfl_up(upto, off, 64);
+            if (lane >= off) upto += up;
+        }
+        count[w][lane] = upto - own;
+        double q = prob[w][lane];
+#pragma unroll
+        for (int off = 32; off > 0; off >>= 1) q += __shfl_xor(q, off, 64);
+        if (lane == 63 && mine < c.experts) {
+            gst(c.counts + mine, upto);
+            gst(s.total + mine, q);
+        }
+    }
+    __syncthreads();
+    if (e >= c.experts) return;
+    n = count[x][run];
+    for (int b = b0; b < b1; ++b) {
+        gst(s.base + (int64_t)b * c.experts + e, n);
+        n += gld(s.hist + (int64_t)b * c.experts + e);
+    }
+}
+
+// A row for every choice; the first workgroup also writes offsets and losses.
+__global__ __launch_bounds__(kThreads) void router_rows_kernel(RouterCall c, RouterSpace s) {
+    extern __shared__ __align__(16) char lds[];
+    __shared__ double red[kWaves];
+    __shared__ int32_t wave_sum[kWaves];
+    const RouterLds m(lds, c.experts, c.top_k);
+    const int token0 = blockIdx.x * kRouterTokens, tokens = min(kRouterTokens, c.tokens - token0);
+    for (int e = threadIdx.x; e < c.experts; e += kThreads) {
+        m.mask[e] = 0;
+        m.first[e] = gld(c.counts + e);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < tokens * c.top_k; i += kThreads) {
+        const int e = gld(c.chosen + (int64_t)token0 * c.top_k + i);
+        m.chosen[i] = e;
+        if (e >= 0) atomicOr(m.mask + e, 1ull << ((uint32_t)i / (uint32_t)c.top_k));
+    }
+    prefix_counts(m.first, c.experts, wave_sum);  // (its barriers also order the masks)
+    const int32_t all = m.first[c.experts];
+    if (blockIdx.x == 0) {
+        double balance = 0.0, lse2 = 0.0, live = 0.0;
+        for (int e = threadIdx.x; e < c.experts; e += kThreads)
+            balance = fma((double)gld(c.counts + e), gld(s.total + e), balance);
+        for (int b = threadIdx.x; b < s.blocks; b += kThreads) {
+            lse2 += gld(s.lse + b);
+            live += gld(s.live + b);
+        }
+        balance = add_up(balance, red);
+        lse2 = add_up(lse2, red);
+        live = add_up(live, red);
+        if (threadIdx.x == 0) put_losses(c, balance, all, lse2, (int32_t)live);
+        for (int e = threadIdx.x; e <= c.experts; e += kThreads) gst(c.offsets + e, m.first[e]);
+        __syncthreads();
+    }
+    if (!c.rows && !c.order) return;
+    for (int e = threadIdx.x; e < c.experts; e += kThreads)
+        m.first[e] += gld(s.base + (int64_t)blockIdx.x * c.experts + e);
+    __syncthreads();
+    put_rows(c, m.mask, m.first, all, token0, tokens, m.chosen);
+}
+
+template <bool BF, int L, int C>
+__global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradCall c) {
+    __shared__ double red[kWaves];
+    constexpr int TEAMS = 64 / L, V = BF ? 8 : 4;
+    const int lane = threadIdx.x & 63, l = lane % L, team = lane / L, wave = threadIdx.x >> 6;
+    const float n = (float)max(gld(c.live), 1);
+    // every token's gradient of the balance loss by its probabilities
+    double choices = 0.0;
+    for (int e = threadIdx.x; e < c.experts; e += kThreads) choices += gld(c.counts + e);
+    choices = add_up(choices, red);
+    float share[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int e = l * C + i;
+        share[i] = e < c.experts && choices > 0.0
+                       ? (float)((double)c.balance * c.experts / n * (gld(c.counts + e) / choices)) : 0.f;
+    }
+    const float zn = 2.f * c.z / n;
+    for (int64_t first = ((int64_t)blockIdx.x * kWaves + wave) * TEAMS; first < c.tokens;
+         first += (int64_t)gridDim.x * kWaves * TEAMS) {
+        const int64_t t = first + team;
+        const bool has = t < c.tokens;
+        const void* row = c.logits;
+        const int64_t at = (has ? t : 0) * c.ld;
+        float z[C], p[C], g[C], add[C];
+        load_logits<BF, C>(row, at + l * C, has ? c.experts - l * C : 0, z);
+        const Softmax x = softmax<L, C>(z, p);
+        const float inv = x.live ? 1.f / x.total : 0.f;
+        const float lse = x.live ? x.top + logf(x.total) : 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            p[i] *= inv;
+            g[i] = share[i];
+            add[i] = 0.f;
+        }
+        if (c.dgates && has) {
+            const int32_t* chosen = c.chosen + t * c.top_k;
+            const float* d = c.dgates + t * c.top_k;
+            // renormalised gates are a softmax over the chosen logits
+            float top = -INFINITY, sum = 0.f, dot = 0.f;
+            auto logit = [&](int e) {
+                return BF ? bf16_bits_to_f32(gld(reinterpret_cast<const uint16_t*>(row) + at + e))
+                          : gld(reinterpret_cast<const float*>(row) + at + e);
+            };
+            auto is = [&](int e) { return e >= 0 && e < c.experts; };
+            if (c.renormalize) {
+                for (int j = 0; j < c.top_k; ++j) {
+                    const int e = gld(chosen + j);
+                    if (is(e)) top = fmaxf(top, logit(e));
+                }
+                for (int j = 0; j < c.top_k; ++j) {
+                    const int e = gld(chosen + j);
+                    if (!is(e)) continue;
+                    const float w = expf(logit(e) - top);
+                    sum += w;
+                    dot = fmaf(w, gld(d + j), dot);
+                }
+                dot /= sum;
+            }
+            for (int j = 0; j < c.top_k; ++j) {
+                const int e = gld(chosen + j);
+                if (!is(e)) continue;
+                const float v = gld(d + j);
+                const float w = c.renormalize ? expf(logit(e) - top) / sum * (v - dot) : v;
+#pragma unroll
+                for (int i = 0; i < C; ++i)
+                    if (l * C + i == e) (c.renormalize ? add[i] : g[i]) += w;
+            }
+        }
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < C; ++i) dot = fmaf(p[i], g[i], dot);
+        dot = team_sum<L>(dot);
+        float o[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[i] = fmaf(p[i], g[i] - dot + zn * lse, add[i]);
+        if (has)
+#pragma unroll
+            for (int q = 0; q < C; q += V)
+                store_unit<V, BF, false>(c.dlogits, t * c.ld_out + l * C + q, c.experts - l * C - q, o + q);
+    }
+}
+
+// Calls fn(lanes of a team, logits a lane).
+template <class F>
+hipError_t with_team(int experts, F&& fn) {
+    using std::integral_constant;
+#define MUON_TEAM(L, C) fn(integral_constant<int, L>{}, integral_constant<int, C>{})
+    if (experts <= 8) return MUON_TEAM(1, 8);
+    if (experts <= 16) return MUON_TEAM(2, 8);
+    if (experts <= 32) return MUON_TEAM(4, 8);
+    if (experts <= 64) return MUON_TEAM(8, 8);
+    if (experts <= 128) return MUON_TEAM(16, 8);
+    if (experts <= 256) return MUON_TEAM(32, 8);
+    if (experts <= 512) return MUON_TEAM(64, 8);
+    return MUON_TEAM(64, 16);
+#undef MUON_TEAM
+}
+
+template <bool BF>
+hipError_t choose(const RouterCall& c, const RouterSpace& s, hipStream_t st) {
+    const size_t lds = router_lds(c.experts, c.top_k);
+    return with_team(c.experts, [&](auto l, auto n) {
+        if (c.tokens <= kRouterTokens)
+            router_choose_kernel<BF, l.value, n.value, true><<<1, kThreads, lds, st>>>(c, s);
+        else
+            router_choose_kernel<BF, l.value, n.value, false><<<s.blocks, kThreads, lds, st>>>(c, s);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+hipError_t launch_router(const RouterCall& c, const RouterSpace& s, hipStream_t st) {
+    hipError_t e = c.bf16 ? choose<true>(c, s, st) : choose<false>(c, s, st);
+    if (e != hipSuccess || c.tokens <= kRouterTokens) return e;
+    router_join_kernel<<<(c.experts + kJoinExperts - 1) / kJoinExperts, 1024, 0, st>>>(c, s);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    router_rows_kernel<<<s.blocks, kThreads, router_lds(c.experts, c.top_k), st>>>(c, s);
+    return hipGetLastError();
+}
+
+hipError_t launch_router_grad(const RouterGradCall& c, int cus, hipStream_t st) {
+    auto go = [&](auto bf) {
+        return with_team(c.experts, [&](auto l, auto n) {
+            const int each = kWaves * (64 / l.value);
+            const int64_t need = ((int64_t)c.tokens + each - 1) / each, most = (int64_t)cus * 8;
+            const int blocks = (int)(need < most ? need : most);
+            router_grad_kernel<bf.value, l.value, n.value><<<blocks, kThreads, 0, st>>>(c);
+            return hipGetLastError();
+        });
+    };
+    return c.bf16 ? go(std::true_type{}) : go(std::false_type{});
+}
+
+}  // namespace muon

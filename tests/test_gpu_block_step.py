@@ -1,0 +1,263 @@
+"""One block of a model as a user runs it: layer norm in front of a query, a key
+and a router projection; the heads' norm and rotary positions into the largest
+logits; the router's groups through the experts' products; everything back to
+gradients, one norm over them, and both steps.  Against the same block in 64
+bits, differentiated by torch; and the library's calls captured in a graph."""
+
+import pytest
+import torch
+
+import muon_step_02_amd as mu
+import oracle
+import synth
+from harness import Handle, TOL_STATE, f64, hp_from, relF
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+T, D, E, K, N = 300, 256, 12, 3, 128
+HEADS, KV, HEAD = 4, 2, 64
+EPS, BALANCE, Z = 1e-5, 0.02, 0.003
+SEQ = [0, 40, 41, 300]
+
+
+class Block:
+    def __init__(self, seed=0):
+        g = torch.Generator(device=DEV).manual_seed(seed)
+
+        def rnd(*s, std=1.0):
+            return torch.randn(*s, generator=g, device=DEV) * std
+
+        def zeros(*s, dtype=torch.float32):
+            return torch.zeros(*s, device=DEV, dtype=dtype)
+
+        h = self.h = Handle.get()
+        self.x = rnd(T, D)
+        # weights by name; what Muon takes and what AdamW takes
+        self.w = dict(q=rnd(HEADS * HEAD, D, std=0.06), k=rnd(KV * HEAD, D, std=0.06), router=rnd(E, D, std=0.1),
+                      norm=1 + rnd(D, std=0.1), bias=rnd(D, std=0.1), qnorm=1 + rnd(HEAD, std=0.1),
+                      knorm=1 + rnd(HEAD, std=0.1))
+        self.W = rnd(E, N, D, std=0.06)
+        self.g = {n: zeros(*t.shape) for n, t in self.w.items()}
+        self.G = zeros(E, N, D)
+        # the gradients that come from behind the block
+        self.dout, self.dq, self.dk = rnd(T, N, std=0.1), rnd(T, HEADS, HEAD, std=0.1), rnd(T, KV, HEAD, std=0.1)
+        self.positions = torch.cat([torch.arange(b - a) for a, b in zip(SEQ, SEQ[1:])]).int().to(DEV)
+        self.cu = torch.tensor(SEQ, dtype=torch.int32, device=DEV)
+        self.freq = mu.muon_rotary_frequencies(HEAD // 2, scaling="linear", factor=2.0).to(DEV)
+        self.y, self.dy, self.dx = zeros(T, D), zeros(T, D), zeros(T, D)
+        self.mean, self.rstd = zeros(T), zeros(T)
+        self.qkv = zeros(T, HEADS + KV, HEAD)                    # one fused tensor, heads of q and k beside each other
+        self.dqkv = zeros(T, HEADS + KV, HEAD)
+        self.qn, self.kn = zeros(T, HEADS, HEAD), zeros(T, KV, HEAD)
+        self.qr, self.kr = zeros(T, HEADS), zeros(T, KV)
+        self.smax = zeros(HEADS)
+        i32 = torch.int32
+        self.logits, self.dlogits = zeros(T, E), zeros(T, E)
+        self.chosen, self.rows = zeros(T, K, dtype=i32), zeros(T, K, dtype=i32)
+        self.order, self.counts = zeros(T * K, dtype=i32), zeros(E, dtype=i32)
+        self.offsets, self.live = zeros(E + 1, dtype=i32), zeros(1, dtype=i32)
+        self.gates, self.dgates, self.losses = zeros(T, K), zeros(T, K), zeros(2)
+        self.xr, self.dxr, self.yr, self.dyr = zeros(T * K, D), zeros(T * K, D), zeros(T * K, N), zeros(T * K, N)
+        self.norm, self.scale = zeros(1), zeros(1)
+        self.ex, self.dex = mu.muon_experts(list(self.W)), mu.muon_experts(list(self.G))
+
+        def space(n):
+            return torch.empty(n, dtype=torch.uint8, device=DEV)
+
+        self.ws_r = space(mu.muon_router_workspace_size(h, self.logits, K))
+        self.ws_n = space(mu.muon_layernorm_workspace_size(h, self.x))
+        self.ws_q = space(mu.muon_layernorm_workspace_size(h, self.qn))
+        self.ws_s = space(mu.muon_qk_smax_workspace_size(h, self.qn, self.kn, self.cu))
+        self.grads = [mu.muon_grad(t) for t in list(self.g.values()) + list(self.G)]
+        self.ws_g = space(mu.muon_grad_workspace_size(h, self.grads))
+        self.hp, self.ahp = hp_from(synth.MUON_DEFAULT), mu.adamw_hparams(step=1, **synth.ADAMW_DEFAULT)
+        self.M = zeros(E, N, D)
+        self.mats = [mu.muon_matrix(*t) for t in zip(self.W, self.G, self.M)]
+        self.ws = space(mu.muon_workspace_size(h, self.mats, self.hp))
+        self.small = ("norm", "bias", "qnorm", "knorm")
+        self.m = {n: (torch.zeros_like(self.w[n]), torch.zeros_like(self.w[n])) for n in self.small}
+        self.ts = [mu.adamw_tensor(self.w[n], self.g[n], *self.m[n]) for n in self.small]
+
+    def front(self):
+        h = self.h
+        mu.muon_layernorm_forward(h, self.x, self.y, self.w["norm"], self.w["bias"], self.mean, self.rstd, EPS)
+
+    def attention(self):
+        h, q, k = self.h, self.qkv[:, :HEADS], self.qkv[:, HEADS:]
+        for t, out, w, r in ((q, self.qn, "qnorm", self.qr), (k, self.kn, "knorm", self.kr)):
+            mu.muon_layernorm_forward(h, t, out, self.w[w], rstd=r, eps=EPS, center=False)
+        mu.muon_rotary(h, [self.qn, self.kn], [self.qn, self.kn], self.positions, self.freq)
+        mu.muon_qk_smax(h, self.qn, self.kn, self.cu, self.cu, self.smax, self.ws_s)
+
+    def route(self):
+        mu.muon_router_forward(self.h, self.logits, self.chosen, self.gates, self.counts, self.offsets, self.ws_r,
+                               rows=self.rows, order=self.order, live=self.live, losses=self.losses, renormalize=True)
+
+    def experts(self):
+        # every token has K choices here: every row is one
+        torch.index_select(self.y, 0, self.order // K, out=self.xr)
+        mu.muon_expert_forward(self.h, self.ex, self.offsets, self.xr, self.yr)
+
+    def back(self):
+        h = self.h
+        # through the experts and the gates (each token's gradient times its gate, in the groups' order)
+        mine = self.dout[self.order.long() // K]
+        self.dgates.view(-1)[self.order.long()] = (self.yr * mine).sum(1)
+        self.dyr.copy_(mine * self.gates.view(-1)[self.order.long()][:, None])
+        mu.muon_expert_grad_input(h, self.ex, self.offsets, self.dyr, self.dxr)
+        mu.muon_expert_grad_weight(h, self.dex, self.offsets, self.xr, self.dyr)
+        mu.muon_router_grad(h, self.logits, self.chosen, self.counts, self.live, self.dlogits, self.dgates, BALANCE, Z,
+                            renormalize=True)
+        # through the positions and the heads' norms
+        back = [torch.empty_like(self.dq), torch.empty_like(self.dk)]
+        mu.muon_rotary(h, [self.dq, self.dk], back, self.positions, self.freq, transpose=True)
+        for cut, d, w, r in ((slice(0, HEADS), back[0], "qnorm", self.qr), (slice(HEADS, None), back[1], "knorm", self.kr)):
+            mu.muon_layernorm_grad(h, self.qkv[:, cut], d, r, self.ws_q, weight=self.w[w], dx=self.dqkv[:, cut],
+                                   dweight=self.g[w], center=False)
+        flat = self.dqkv.view(T, -1)
+        torch.mm(flat[:, :HEADS * HEAD].t(), self.y, out=self.g["q"])
+        torch.mm(flat[:, HEADS * HEAD:].t(), self.y, out=self.g["k"])
+        torch.mm(self.dlogits.t(), self.y, out=self.g["router"])
+        self.dy.copy_(self.dxr[self.rows.long()].sum(1) + self.dlogits @ self.w["router"]
+                      + flat @ torch.cat([self.w["q"], self.w["k"]]))
+        mu.muon_layernorm_grad(h, self.x, self.dy, self.rstd, self.ws_n, mean=self.mean, weight=self.w["norm"], dx=self.dx,
+                               dweight=self.g["norm"], dbias=self.g["bias"])
+
+    def step(self):
+        mu.muon_grad_norm(self.h, self.grads, 1.0, self.ws_g, norm_out=self.norm, scale_out=self.scale)
+        mu.muon_step_batched_scaled(self.h, self.mats, self.hp, self.scale, self.ws)
+        mu.adamw_step_scaled(self.h, self.ts, self.ahp, self.scale)
+
+    def forward(self):
+        self.front()
+        self.qkv.copy_((self.y @ torch.cat([self.w["q"], self.w["k"]]).t()).view(T, HEADS + KV, HEAD))
+        torch.mm(self.y, self.w["router"].t(), out=self.logits)
+        self.attention()
+        self.route()
+        self.experts()
+
+
+def _reference(b):
+    """The same in 64 bits; the choices as the library made them."""
+    w = {n: t.double().clone().requires_grad_(True) for n, t in b.w.items()}
+    W, x = b.W.double().clone().requires_grad_(True), b.x.double().clone().requires_grad_(True)
+    y = torch.nn.functional.layer_norm(x, (D,), w["norm"], w["bias"], EPS)
+
+    def heads(p, scale, n):
+        t = (y @ p.t()).view(T, n, HEAD)
+        t = t * (t.square().mean(-1, keepdim=True) + EPS).rsqrt() * scale
+        a = (b.positions.double()[:, None] * b.freq)[:, None, :]
+        u, v = t[..., :HEAD // 2], t[..., HEAD // 2:]
+        return torch.cat([u * a.cos() - v * a.sin(), v * a.cos() + u * a.sin()], -1)
+
+    q, k = heads(w["q"], w["qnorm"], HEADS), heads(w["k"], w["knorm"], KV)
+    z = y @ w["router"].t()
+    p = z.softmax(1)
+    chosen = b.chosen.long()
+    gates = p.gather(1, chosen)
+    gates = gates / gates.sum(1, keepdim=True)
+    out = sum(gates[:, j:j + 1] * (W[chosen[:, j]] @ y[:, :, None])[:, :, 0] for j in range(K))
+    share = torch.bincount(chosen.view(-1), minlength=E).double() / (T * K)
+    balance, zl = E * (share * p.mean(0)).sum(), torch.logsumexp(z, 1).square().mean()
+    loss = (out * b.dout.double()).sum() + (q * b.dq.double()).sum() + (k * b.dk.double()).sum() \
+        + BALANCE * balance + Z * zl
+    loss.backward()
+    return dict(y=y, q=q, k=k, z=z, gates=gates, losses=torch.stack([balance, zl]), out=out), w, W, x
+
+
+# A chain of up to five fp32 sums of at most 300 products each: a sum's relative
+# error is at most 302 * 2^-24, times the sum of magnitudes over the sum, which
+# for products of random signs is about sqrt(300).
+TOL = 5 * 302 * 2.0 ** -24 * 17.4
+
+
+def test_block_against_64_bits():
+    b = Block()
+    b.forward()
+    b.back()
+    torch.cuda.synchronize()
+    got, w, W, x = _reference(b)
+    top = torch.sort(got["z"], dim=1, descending=True, stable=True)
+    # the library's choices are those of its own logits, which are next to these
+    margin = (top.values[:, K - 1] - top.values[:, K]) > 1e-3
+    assert torch.equal(b.chosen.long().sort(1).values[margin], top.indices[:, :K].sort(1).values[margin])
+    for mine, name in ((b.y, "y"), (b.qn, "q"), (b.kn, "k"), (b.logits, "z"), (b.gates, "gates"), (b.losses, "losses")):
+        assert relF(f64(mine), f64(got[name])) <= TOL, name
+    out = (b.yr[b.rows.long()] * b.gates[:, :, None]).sum(1)
+    assert relF(f64(out), f64(got["out"])) <= TOL
+    assert relF(f64(b.G), f64(W.grad)) <= TOL and relF(f64(b.dx), f64(x.grad)) <= TOL
+    for n in b.w:
+        assert relF(f64(b.g[n]), f64(w[n].grad)) <= TOL, n
+    # the largest logits of the turned heads
+    q, k = f64(b.qn), f64(b.kn)
+    for hd in range(HEADS):
+        best = max((q[i, hd] @ k[a:i + 1, hd * KV // HEADS].T).max() for a, e in zip(SEQ, SEQ[1:]) for i in range(a, e))
+        assert abs(float(b.smax[hd]) - best / 8) <= 66 * 2.0 ** -23 * abs(q).max() * abs(k).max() * 8
+    # one norm over all of it, and AdamW's tensors stepped with its scale
+    before = {n: f64(b.w[n]) for n in b.small}
+    b.step()
+    torch.cuda.synchronize()
+    clipped, norm = oracle.clip_by_global_norm([f64(t) for t in list(b.g.values()) + list(b.G)], 1.0)
+    assert abs(float(b.norm) - norm) <= 1e-7 * norm
+    for n, g in zip(b.w, clipped):
+        if n in b.small:
+            th, m, v = oracle.adamw_tensor_step(before[n], g, 0.0 * g, 0.0 * g, step=1, **synth.ADAMW_DEFAULT)
+            assert relF(f64(b.w[n]), th) <= TOL_STATE and relF(f64(b.m[n][0]), m) <= TOL_STATE
+
+
+def test_captured_calls_replay_as_the_eager_ones():
+    a, b = Block(5), Block(5)
+    a.forward()
+    b.forward()
+    a.back()
+    b.back()
+    torch.cuda.synchronize()
+
+    def calls(s):
+        s.front()
+        s.attention()
+        s.route()
+        mu.muon_expert_forward(s.h, s.ex, s.offsets, s.xr, s.yr)
+        mu.muon_router_grad(s.h, s.logits, s.chosen, s.counts, s.live, s.dlogits, s.dgates, BALANCE, Z, renormalize=True)
+        mu.muon_layernorm_grad(s.h, s.x, s.dy, s.rstd, s.ws_n, mean=s.mean, weight=s.w["norm"], dx=s.dx,
+                               dweight=s.g["norm"], dbias=s.g["bias"], accumulate=True)
+        s.step()
+
+    names = ("y", "qn", "kn", "smax", "chosen", "gates", "rows", "order", "counts", "offsets", "losses", "yr", "dlogits", "dx",
+             "norm", "scale", "W", "M")
+    g, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(g, stream=side):
+        calls(a)
+    for r in range(4):
+        g.replay()
+        calls(b)
+        torch.cuda.synchronize()
+        for n in names:
+            assert torch.equal(getattr(a, n), getattr(b, n)), (r, n)
+        for n in a.w:
+            assert torch.equal(a.w[n], b.w[n]) and torch.equal(a.g[n], b.g[n]), (r, n)
+        for s in (a, b):   # another batch for the next one, with some tokens padded
+            s.x.mul_(-0.5).add_(0.1 * r)
+            s.qkv.mul_(1.5)
+            s.logits.add_(s.logits.flip(0), alpha=0.5)
+            s.logits[T - 7 * r:] = -float("inf")
+            s.positions.add_(1000 * r)
+        torch.cuda.synchronize()
+
+
+def test_two_handles_on_two_streams():
+    a, b = Block(6), Block(6)
+    b.h = mu.muon_init(0)
+    try:
+        s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        for s, block in ((s1, a), (s2, b)):
+            with torch.cuda.stream(s):
+                block.forward()
+                block.back()
+        torch.cuda.synchronize()
+        for n in ("y", "qn", "smax", "chosen", "rows", "order", "losses", "yr", "dlogits", "dqkv", "dx", "G"):
+            assert torch.equal(getattr(a, n), getattr(b, n)), n
+    finally:
+        mu.muon_destroy(b.h)
