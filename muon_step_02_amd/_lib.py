@@ -765,6 +765,20 @@ def muon_qk_smax(h, q, k, cu_q, cu_k, smax_q, workspace, smax_k=None, scale=None
                                _stream_on(stream, dev, h)), "muon_qk_smax")
 
 
+def _queue(h, stream, *tensors):
+    """The stream to launch on, once every tensor (None among them: not given) is
+    known to be on the handle's device.  (One look at each: a small call's time is
+    the host's.)"""
+    i = h.device
+    for t in tensors:
+        if t is not None and t.get_device() != i:
+            _stream_on(stream, _same_device(*tensors), h)  # says which of them is where
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(i)
+    return _stream_on(stream, tensors[0].device, h)
+
+
 def _heads(t, what):
     """Descriptor of a (tokens, heads, width) tensor, or of a (tokens, width)
     one as one head a token."""
@@ -774,7 +788,7 @@ def _heads(t, what):
         s, sh, sw = t.stride()
     elif n == 2:
         (tokens, width), heads = t.shape, 1
-        (s, sw), sh = t.stride(), width
+        s, sw = t.stride()
     else:
         raise ValueError("%s must be (tokens, heads, width) or (tokens, width)" % what)
     if sw != 1 and width > 1:
@@ -791,18 +805,18 @@ def _vector(t, numel, dtype, what):
     """Pointer of a contiguous tensor of `numel` values (None: not given)."""
     if t is None:
         return None
-    if t.numel() != numel or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
-        raise ValueError("%s must be contiguous, %d values%s" % (what, numel, "" if dtype is None else " of %s" % dtype))
+    if t.numel() != numel or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s must be contiguous, %d values of %s" % (what, numel, dtype))
     return t.data_ptr()
 
 
-def _layernorm(x, weight, bias, center, eps):
-    cols = x.shape[-1]
-    if weight is not None and bias is not None and weight.dtype != bias.dtype:
-        raise TypeError("weight and bias differ in type")
-    w = weight if weight is not None else bias
-    return MuonLayernorm(_vector(weight, cols, None, "weight"), _vector(bias, cols, None, "bias"), x.shape[0], cols,
-                         _dt(x), _dt(w) if w is not None else MUON_F32, 1 if center else 0, eps)
+def _pair(a, b, numel, what):
+    """(pointer, pointer, type) of two vectors of one type, either may be None."""
+    t = a if a is not None else b
+    if t is None:
+        return None, None, MUON_F32
+    dtype = t.dtype
+    return _vector(a, numel, dtype, what), _vector(b, numel, dtype, what), _dt(t)
 
 
 def muon_layernorm_forward(h, x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5, center=True,
@@ -813,20 +827,22 @@ def muon_layernorm_forward(h, x, y, weight=None, bias=None, mean=None, rstd=None
     row; optional) receive the statistics that :func:`muon_layernorm_grad` reads.
     Without ``center`` the mean is taken as zero (root mean square norm)."""
     import torch
-    dev = _same_device(x, y, weight, bias, mean, rstd)
-    if y.shape != x.shape or y.dtype != x.dtype:
+    queue = _queue(h, stream, x, y, weight, bias, mean, rstd)
+    shape = x.shape
+    if y.shape != shape or y.dtype != x.dtype:
         raise ValueError("x and y differ in shape or type")
-    n, hx, hy = _layernorm(x, weight, bias, center, eps), _heads(x, "x"), _heads(y, "y")
-    rows = x.shape[0] * hx.heads
-    _check(load().muon_layernorm_forward(h, n, hx, hy, _vector(mean, rows, torch.float32, "mean"),
-                                         _vector(rstd, rows, torch.float32, "rstd"), _stream_on(stream, dev, h)),
-           "muon_layernorm_forward")
+    hx, hy, cols = _heads(x, "x"), _heads(y, "y"), shape[-1]
+    pw, pb, wide = _pair(weight, bias, cols, "weight and bias")
+    rows, f32 = shape[0] * hx.heads, torch.float32
+    n = MuonLayernorm(pw, pb, shape[0], cols, _dt(x), wide, 1 if center else 0, eps)
+    _check(load().muon_layernorm_forward(h, n, hx, hy, _vector(mean, rows, f32, "mean"),
+                                         _vector(rstd, rows, f32, "rstd"), queue), "muon_layernorm_forward")
 
 
 def muon_layernorm_workspace_size(h, x):
     """Workspace bytes of :func:`muon_layernorm_grad` for an ``x`` of this shape and type."""
     sz = ctypes.c_size_t()
-    n = _layernorm(x, None, None, True, 0.0)
+    n = MuonLayernorm(None, None, x.shape[0], x.shape[-1], _dt(x), MUON_F32, 1, 0.0)
     _check(load().muon_layernorm_workspace_size(h, n, _heads(x, "x").heads, sz), "muon_layernorm_workspace_size")
     return sz.value
 
@@ -838,22 +854,22 @@ def muon_layernorm_grad(h, x, dy, rstd, workspace, mean=None, weight=None, dx=No
     ``dweight`` and ``dbias`` of one type, added to what they hold with
     ``accumulate``.  Each is optional."""
     import torch
-    dev = _same_device(x, dy, rstd, workspace, mean, weight, dx, dweight, dbias)
+    queue = _queue(h, stream, x, dy, rstd, workspace, mean, weight, dx, dweight, dbias)
+    shape, dtype = x.shape, x.dtype
     for t in (dy, dx):
-        if t is not None and (t.shape != x.shape or t.dtype != x.dtype):
+        if t is not None and (t.shape != shape or t.dtype != dtype):
             raise ValueError("x, dy and dx differ in shape or type")
-    if dweight is not None and dbias is not None and dweight.dtype != dbias.dtype:
-        raise TypeError("dweight and dbias differ in type")
-    n, hx, hdy = _layernorm(x, weight, None, center, 0.0), _heads(x, "x"), _heads(dy, "dy")
-    rows, cols = x.shape[0] * hx.heads, x.shape[-1]
     if center and mean is None:
         raise ValueError("a centered norm needs its mean")
-    g = dweight if dweight is not None else dbias
+    hx, cols, f32 = _heads(x, "x"), shape[-1], torch.float32
+    rows = shape[0] * hx.heads
+    pw, _, wide = _pair(weight, None, cols, "weight")
+    pdw, pdb, grad = _pair(dweight, dbias, cols, "dweight and dbias")
+    n = MuonLayernorm(pw, None, shape[0], cols, _dt(x), wide, 1 if center else 0, 0.0)
     _check(load().muon_layernorm_grad(
-        h, n, hx, hdy, _vector(mean, rows, torch.float32, "mean"), _vector(rstd, rows, torch.float32, "rstd"),
-        _heads(dx, "dx") if dx is not None else None, _vector(dweight, cols, None, "dweight"),
-        _vector(dbias, cols, None, "dbias"), _dt(g) if g is not None else MUON_F32, 1 if accumulate else 0,
-        workspace.data_ptr(), _nbytes(workspace), _stream_on(stream, dev, h)), "muon_layernorm_grad")
+        h, n, hx, _heads(dy, "dy"), _vector(mean, rows, f32, "mean"), _vector(rstd, rows, f32, "rstd"),
+        _heads(dx, "dx") if dx is not None else None, pdw, pdb, grad, 1 if accumulate else 0, workspace.data_ptr(),
+        _nbytes(workspace), queue), "muon_layernorm_grad")
 
 
 def muon_rotary_frequencies(pairs, base=10000.0, scaling="none", factor=1.0, context=0.0, low=1.0, high=32.0):
@@ -882,20 +898,21 @@ def muon_rotary(h, x, y, positions, frequencies, first=0, interleaved=False, sca
     n = len(xs)
     if n != len(ys) or not 1 <= n <= 4:
         raise ValueError("expected one to four tensors and as many outputs")
-    dev = _same_device(positions, frequencies, *xs, *ys)
-    x0 = xs[0]
+    queue = _queue(h, stream, positions, frequencies, *xs, *ys)
+    x0, pairs = xs[0], frequencies.numel()
     tokens, dim, dtype = x0.shape[0], x0.shape[-1], x0.dtype
-    for a, b in zip(xs, ys):
-        if a.shape != b.shape or a.shape[0] != tokens or a.shape[-1] != dim or a.dtype != dtype or b.dtype != dtype:
-            raise ValueError("the tensors differ in tokens, head size or type, or from their outputs in shape")
-    if positions.numel() != tokens:
-        raise ValueError("positions must hold one value per token")
-    pairs = frequencies.numel()
-    p = MuonPositions(_int32(positions, "positions"), _vector(frequencies, pairs, torch.float64, "frequencies"),
-                      tokens, dim, first, pairs, 1 if interleaved else 0, _dt(x0), scale)
     hs = MuonHeads * n
-    _check(load().muon_rotary(h, p, hs(*[_heads(t, "x") for t in xs]), hs(*[_heads(t, "y") for t in ys]), n,
-                              1 if transpose else 0, _stream_on(stream, dev, h)), "muon_rotary")
+    hx, hy = hs(), hs()
+    for i in range(n):
+        a, b = xs[i], ys[i]
+        shape = a.shape
+        if b.shape != shape or shape[0] != tokens or shape[-1] != dim or a.dtype != dtype or b.dtype != dtype:
+            raise ValueError("the tensors differ in tokens, head size or type, or from their outputs in shape")
+        hx[i], hy[i] = _heads(a, "x"), _heads(b, "y")
+    p = MuonPositions(_vector(positions, tokens, torch.int32, "positions"),
+                      _vector(frequencies, pairs, torch.float64, "frequencies"), tokens, dim, first, pairs,
+                      1 if interleaved else 0, _dt(x0), scale)
+    _check(load().muon_rotary(h, p, hx, hy, n, 1 if transpose else 0, queue), "muon_rotary")
 
 
 def _router(logits, top_k, renormalize):
@@ -903,20 +920,19 @@ def _router(logits, top_k, renormalize):
         raise ValueError("logits must be 2D with unit column stride")
     tokens, experts = logits.shape
     return MuonRouter(logits.data_ptr(), tokens, logits.stride(0) if tokens > 1 else experts, experts, top_k,
-                      _dt(logits), 1 if renormalize else 0)
+                      _dt(logits), 1 if renormalize else 0), tokens, experts
 
 
-def _choices(t, tokens, dtype, what):
-    """(pointer, top_k) of a contiguous (tokens, top_k) tensor."""
-    if t.dim() != 2 or t.shape[0] != tokens or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError("%s must be a contiguous (tokens, top_k) tensor of %s" % (what, dtype))
-    return t.data_ptr(), t.shape[1]
+def _top_k(chosen):
+    if chosen.dim() != 2:
+        raise ValueError("chosen must be (tokens, top_k)")
+    return chosen.shape[1]
 
 
 def muon_router_workspace_size(h, logits, top_k):
     """Workspace bytes of :func:`muon_router_forward` for logits of this shape."""
     sz = ctypes.c_size_t()
-    _check(load().muon_router_workspace_size(h, _router(logits, top_k, False), sz), "muon_router_workspace_size")
+    _check(load().muon_router_workspace_size(h, _router(logits, top_k, False)[0], sz), "muon_router_workspace_size")
     return sz.value
 
 
@@ -932,18 +948,18 @@ def muon_router_forward(h, logits, chosen, gates, counts, offsets, workspace, ro
     have a logit above -inf; ``losses`` (2 float32): the balance and the z loss."""
     import torch
     i32, f32 = torch.int32, torch.float32
-    dev = _same_device(logits, chosen, gates, counts, offsets, workspace, rows, order, live, losses)
-    pc, top_k = _choices(chosen, logits.shape[0], i32, "chosen")
-    r = _router(logits, top_k, renormalize)
-    n = r.tokens * top_k
-    if gates.shape != chosen.shape or (rows is not None and rows.shape != chosen.shape):
+    queue = _queue(h, stream, logits, chosen, gates, counts, offsets, workspace, rows, order, live, losses)
+    top_k, shape = _top_k(chosen), chosen.shape
+    r, tokens, experts = _router(logits, top_k, renormalize)
+    n = tokens * top_k
+    if gates.shape != shape or (rows is not None and rows.shape != shape):
         raise ValueError("chosen, gates and rows differ in shape")
-    out = MuonRouting(pc, _vector(gates, n, f32, "gates"), _vector(counts, r.experts, i32, "counts"),
-                      _vector(offsets, r.experts + 1, i32, "offsets"), _vector(rows, n, i32, "rows"),
-                      _vector(order, n, i32, "order"), _vector(live, 1, i32, "live"),
+    out = MuonRouting(_vector(chosen, n, i32, "chosen"), _vector(gates, n, f32, "gates"),
+                      _vector(counts, experts, i32, "counts"), _vector(offsets, experts + 1, i32, "offsets"),
+                      _vector(rows, n, i32, "rows"), _vector(order, n, i32, "order"), _vector(live, 1, i32, "live"),
                       _vector(losses, 2, f32, "losses"))
-    _check(load().muon_router_forward(h, r, out, workspace.data_ptr(), _nbytes(workspace),
-                                      _stream_on(stream, dev, h)), "muon_router_forward")
+    _check(load().muon_router_forward(h, r, out, workspace.data_ptr(), _nbytes(workspace), queue),
+           "muon_router_forward")
 
 
 def muon_router_grad(h, logits, chosen, counts, live, dlogits, dgates=None, balance=0.0, z=0.0,
@@ -951,17 +967,17 @@ def muon_router_grad(h, logits, chosen, counts, live, dlogits, dgates=None, bala
     """``dlogits`` of sum(``dgates`` * gates) + ``balance`` * balance loss + ``z`` * z
     loss, with what :func:`muon_router_forward` gave."""
     import torch
-    dev = _same_device(logits, chosen, counts, live, dlogits, dgates)
-    pc, top_k = _choices(chosen, logits.shape[0], torch.int32, "chosen")
-    r = _router(logits, top_k, renormalize)
-    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or \
-            (r.experts > 1 and dlogits.stride(1) != 1):
+    i32 = torch.int32
+    queue = _queue(h, stream, logits, chosen, counts, live, dlogits, dgates)
+    top_k = _top_k(chosen)
+    r, tokens, experts = _router(logits, top_k, renormalize)
+    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or (experts > 1 and dlogits.stride(1) != 1):
         raise ValueError("dlogits must have the logits' shape and type, and unit column stride")
-    _check(load().muon_router_grad(h, r, pc, _vector(counts, r.experts, torch.int32, "counts"),
-                                   _vector(live, 1, torch.int32, "live"),
-                                   _vector(dgates, r.tokens * top_k, torch.float32, "dgates"), balance, z,
-                                   dlogits.data_ptr(), dlogits.stride(0) if r.tokens > 1 else r.experts,
-                                   _stream_on(stream, dev, h)), "muon_router_grad")
+    n = tokens * top_k
+    _check(load().muon_router_grad(h, r, _vector(chosen, n, i32, "chosen"), _vector(counts, experts, i32, "counts"),
+                                   _vector(live, 1, i32, "live"), _vector(dgates, n, torch.float32, "dgates"), balance,
+                                   z, dlogits.data_ptr(), dlogits.stride(0) if tokens > 1 else experts, queue),
+           "muon_router_grad")
 
 
 def muon_test_gram_bf16(h, X, A, m, n, ldx, lda, s2=1.0, stream=None):

@@ -66,7 +66,7 @@ hipError_t launch_rotary(const RotaryCall& c, hipStream_t st);
 // ---- router ----------------------------------------------------------------------
 constexpr int kRouterMaxExperts = 1024;  // as many as the products take
 constexpr int kRouterMaxChoices = 32;
-constexpr int64_t kRouterMaxTokens = (int64_t)1 << 28;  // 2^22 workgroups of 256 threads
+constexpr int64_t kRouterMaxTokens = (int64_t)1 << 28;  // 2^22 workgroups of 512 threads
 constexpr int kRouterTokens = 64;  // of a workgroup: one bit each in an expert's mask
 
 struct RouterCall {

@@ -34,9 +34,8 @@ namespace muon {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
-constexpr int kNone = 0x7fffffff;
 
 // A token's logits over the L lanes of a team: lane l holds C from l * C on,
 // -inf behind the last.
@@ -81,56 +80,51 @@ __device__ __forceinline__ Softmax softmax(const float* z, float* e) {
     return s;
 }
 
-// The largest of the team's logits and its index, the lowest among equals;
-// kNone where none is above -inf.
-template <int HALF>
-__device__ __forceinline__ void best_step(float& v, int& i) {
-    float ov;
-    int oi;
-    if constexpr (HALF >= 16) {
-        // each lane of a half sees the other half's pair: the two outputs hold
-        // both halves in every lane, and the better one of the two is the same
-        const uint32_t b = __builtin_bit_cast(uint32_t, v);
-        const auto s = HALF == 16 ? __builtin_amdgcn_permlane16_swap(b, b, false, false)
-                                  : __builtin_amdgcn_permlane32_swap(b, b, false, false);
-        const auto t = HALF == 16 ? __builtin_amdgcn_permlane16_swap((uint32_t)i, (uint32_t)i, false, false)
-                                  : __builtin_amdgcn_permlane32_swap((uint32_t)i, (uint32_t)i, false, false);
-        v = __builtin_bit_cast(float, (uint32_t)s[0]);
-        i = (int)t[0];
-        ov = __builtin_bit_cast(float, (uint32_t)s[1]);
-        oi = (int)t[1];
-    } else {
-        constexpr int ctrl = HALF == 1 ? 0xb1 : HALF == 2 ? 0x4e : HALF == 4 ? 0x141 : 0x140;
-        ov = __builtin_bit_cast(float, lane_move<ctrl>(__builtin_bit_cast(uint32_t, v)));
-        oi = (int)lane_move<ctrl>((uint32_t)i);
-    }
-    if (ov > v || (ov == v && oi < i)) {
-        v = ov;
-        i = oi;
-    }
+// Logits as whole numbers in their order, both zeros alike: the maximum is one
+// instruction without a look at NaNs, which come last, with what is taken.
+constexpr int32_t kTaken = INT32_MIN;
+constexpr int32_t kLowest = (int32_t)0x807fffff;  // -inf
+__device__ __forceinline__ int32_t key_of(float z) {
+    const int32_t b = __builtin_bit_cast(int32_t, z + 0.f);
+    return z == z ? b ^ ((b >> 31) & 0x7fffffff) : kTaken;
+}
+__device__ __forceinline__ float logit_of(int32_t key) {
+    return __builtin_bit_cast(float, key ^ ((key >> 31) & 0x7fffffff));
 }
 
+// One choice of a team: its largest key, `top` (kLowest or less: none is left),
+// taken out of the lane that holds it, the lowest index first among equals (lane
+// l has the indices from l * C on).  Returns that lane's place of it, or -1.
 template <int L, int C>
-__device__ __forceinline__ void best(const float* z, int first, float& v, int& i) {
-    v = -INFINITY;
-    i = kNone;
+__device__ __forceinline__ int take(int32_t* key, int32_t& top) {
+    int32_t m = key[0];
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-        if (z[c] > v) {
-            v = z[c];
-            i = first + c;
-        }
-    if constexpr (L > 1) best_step<1>(v, i);
-    if constexpr (L > 2) best_step<2>(v, i);
-    if constexpr (L > 4) best_step<4>(v, i);
-    if constexpr (L > 8) best_step<8>(v, i);
-    if constexpr (L > 16) best_step<16>(v, i);
-    if constexpr (L > 32) best_step<32>(v, i);
+    for (int c = 1; c < C; ++c) m = max(m, key[c]);
+    top = team_reduce<L>(m, [](int32_t a, int32_t b) { return max(a, b); });
+    bool left = m == top && top > kLowest;
+    if constexpr (L > 1) {
+        const int lane = threadIdx.x & 63, l = lane % L;
+        const uint64_t equal = __ballot(left);
+        // (a team without one has no bits here, and no lane that is left)
+        if constexpr (L == 64)
+            left = left && l == __builtin_ctzll(equal | 1ull << 63);
+        else
+            left = left && l == __builtin_ctz((uint32_t)(equal >> (lane - l)) | 1u << 31);
+    }
+    int at = -1;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const bool hit = left && key[c] == top;
+        key[c] = hit ? kTaken : key[c];
+        at = hit ? c : at;
+        left = left && !hit;
+    }
+    return at;
 }
 
 // The exclusive prefix sums of n <= 1024 counts, and their sum at [n].
 __device__ __forceinline__ void prefix_counts(int32_t* s, int n, int32_t* wave_sum) {
-    constexpr int Q = kRouterMaxExperts / kThreads;
+    constexpr int Q = kRouterMaxExperts / kThreads;  // counts of a thread
     int v[Q], sum = 0;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
@@ -231,6 +225,7 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
     const int lane = threadIdx.x & 63, l = lane % L, team = lane / L, wave = threadIdx.x >> 6;
     const int token0 = blockIdx.x * kRouterTokens, tokens = min(kRouterTokens, c.tokens - token0);
     for (int e = threadIdx.x; e < c.experts; e += kThreads) m.mask[e] = 0;
+    for (int i = threadIdx.x; i < tokens * c.top_k; i += kThreads) m.chosen[i] = -1;
     __syncthreads();
 
     float probs[C];
@@ -252,28 +247,31 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
             lse2 = fma(lse, lse, lse2);
             ++live;
         }
-        // one choice after the other
-        float sum = 0.f;
-        for (int j = 0; j < c.top_k; ++j) {
-            float v;
-            int i;
-            best<L, C>(z, l * C, v, i);
-            const bool some = i != kNone;
+        // one choice after the other, by the lane that holds it
+        int32_t key[C];
 #pragma unroll
-            for (int k = 0; k < C; ++k)
-                if (l * C + k == i) z[k] = -INFINITY;
-            const float g = some ? expf(v - x.top) : 0.f;
-            sum += g;
-            if (l == 0 && has) {
-                m.chosen[t * c.top_k + j] = some ? i : -1;
-                m.gates[t * c.top_k + j] = g;
-                if (some) atomicOr(m.mask + i, 1ull << t);
+        for (int i = 0; i < C; ++i) key[i] = key_of(z[i]);
+        for (int j = 0; j < c.top_k; ++j) {
+            int32_t top;
+            const int i = take<L, C>(key, top);
+            if (i >= 0) {
+                m.chosen[t * c.top_k + j] = l * C + i;
+                m.gates[t * c.top_k + j] = logit_of(top);
             }
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        // then its gates, by as many lanes as there are
+        float sum = 0.f;
+        for (int j = l; j < c.top_k; j += L) {
+            if (!has) continue;
+            float& g = m.gates[t * c.top_k + j];
+            g = m.chosen[t * c.top_k + j] >= 0 ? expf(g - x.top) : 0.f;
+            sum += g;
+        }
+        if (c.renormalize) sum = team_sum<L>(sum);
         // a NaN logit, which x.total has seen, makes its token's gates NaN
         float by = c.renormalize ? fmaf(0.f, x.total, sum) : x.total;
         if (by == 0.f) by = 1.f;
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         if (has)
             for (int j = l; j < c.top_k; j += L) m.gates[t * c.top_k + j] /= by;
     }
@@ -292,9 +290,12 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
 
     const int64_t at = (int64_t)token0 * c.top_k;
     for (int i = threadIdx.x; i < tokens * c.top_k; i += kThreads) {
-        gst(c.chosen + at + i, m.chosen[i]);
+        const int e = m.chosen[i];
+        if (e >= 0) atomicOr(m.mask + e, 1ull << ((uint32_t)i / (uint32_t)c.top_k));
+        gst(c.chosen + at + i, e);
         gst(c.gates + at + i, m.gates[i]);
     }
+    __syncthreads();
     double balance = 0.0;
     for (int e = threadIdx.x; e < c.experts; e += kThreads) {
         const int n = __popcll(m.mask[e]);

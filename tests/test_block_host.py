@@ -351,7 +351,8 @@ def test_binding_describes_tensors():
         _lib._heads(t.transpose(1, 2), "x")
     with pytest.raises(ValueError):
         _lib._heads(t[0, 0], "x")
-    with pytest.raises(ValueError):
-        _lib._vector(t[:, 0, 0], 6, torch.float32, "w")
+    for bad in (t[:, 0, 0], torch.zeros(5), torch.zeros(6, dtype=torch.float64)):
+        with pytest.raises(ValueError):
+            _lib._vector(bad, 6, torch.float32, "w")
     with pytest.raises(ValueError):
         _lib._router(t[0].t(), 1, False)
