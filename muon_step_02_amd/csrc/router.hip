@@ -9,7 +9,7 @@
 //   z loss = sum_t lse_t^2 / n,   n = tokens with a logit above -inf
 //
 // Three launches.  A workgroup takes 64 tokens, a team of 1 to 64 lanes one of
-// them at a time, with 8 (16 beyond 512 experts) logits a lane in registers.
+// them at a time, with 8 (16 beyond 64 experts) logits a lane in registers.
 // Which of the 64 tokens chose an expert is one 64-bit mask in LDS: its bits
 // count the choices, and those below a token's own are the token's place among
 // them, whatever order the bits were set in.  The second launch adds up the
@@ -25,6 +25,7 @@
 #include <math.h>
 
 #include <type_traits>
+#include <utility>
 
 #include "block.h"
 #include "team.h"
@@ -36,6 +37,11 @@ namespace {
 
 constexpr int kThreads = 512;
 constexpr int kWaves = kThreads / 64;
+
+// e^x for x <= 0 (or NaN) by the base-2 instruction: the product is rounded once
+// more, so the result is off by |x| 2^-24 of itself, as much as the rounding of x
+// = z - top costs already.  Below 2^-126 it is zero.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(x * 1.44269502f); }
 
 // A token's logits over the L lanes of a team: lane l holds C from l * C on,
 // -inf behind the last.
@@ -55,28 +61,24 @@ struct Softmax {
     bool live;
 };
 
-// e = exp(z - top) in place of nothing: z stays.  A token without any logit
-// above -inf gets zeros.
+// e = exp(z - top).  A token without any logit above -inf gets zeros.
 template <int L, int C>
 __device__ __forceinline__ Softmax softmax(const float* z, float* e) {
-    float m = -INFINITY, any = 0.f;
+    float m = z[0];
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        m = fmaxf(m, z[i]);
-        any = z[i] == -INFINITY ? any : 1.f;  // a NaN counts
-    }
+    for (int i = 1; i < C; ++i) m = fmaxf(m, z[i]);  // (of a NaN and a number the number)
     m = team_reduce<L>(m, [](float a, float b) { return fmaxf(a, b); });
-    any = team_reduce<L>(any, [](float a, float b) { return fmaxf(a, b); });
     Softmax s;
-    s.live = any > 0.f;
-    s.top = m;
+    s.live = m != -INFINITY;
+    s.top = s.live ? m : 0.f;
     float t = 0.f;
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        e[i] = s.live ? expf(z[i] - m) : 0.f;
+        e[i] = exp_of(z[i] - s.top);
         t += e[i];
     }
     s.total = team_sum<L>(t);
+    s.live = s.live || s.total != s.total;  // a NaN counts
     return s;
 }
 
@@ -86,7 +88,7 @@ constexpr int32_t kTaken = INT32_MIN;
 constexpr int32_t kLowest = (int32_t)0x807fffff;  // -inf
 __device__ __forceinline__ int32_t key_of(float z) {
     const int32_t b = __builtin_bit_cast(int32_t, z + 0.f);
-    return z == z ? b ^ ((b >> 31) & 0x7fffffff) : kTaken;
+    return b ^ ((b >> 31) & 0x7fffffff);
 }
 __device__ __forceinline__ float logit_of(int32_t key) {
     return __builtin_bit_cast(float, key ^ ((key >> 31) & 0x7fffffff));
@@ -122,6 +124,69 @@ __device__ __forceinline__ int take(int32_t* key, int32_t& top) {
     return at;
 }
 
+// Calls fn(integral_constant<int, 1>) ... fn(integral_constant<int, 15>).
+template <class F, int... I>
+__device__ __forceinline__ void turns_of(F&& fn, std::integer_sequence<int, I...>) {
+    (fn(std::integral_constant<int, I + 1>{}), ...);
+}
+template <class F>
+__device__ __forceinline__ void row_turns(F&& fn) {
+    turns_of(fn, std::make_integer_sequence<int, 15>{});
+}
+
+// Up to kFew choices of a team of 16 lanes or more at once.  Of 16 groups of
+// logits (the lanes' of equal place in their rows of 16) the k largest maxima
+// bound the k-th largest logit from below; what reaches the bound, 8 to 16 logits
+// as a rule, goes side by side to 16 lanes, where each counts those before it.
+// Returns false, for the whole wave, where a team has more than 16 of them.
+// 220 instructions for the wave's teams, where one choice after the other takes
+// 75 each: 25.9 -> XX us for 32768 tokens of 256 experts and 8 choices.
+constexpr int kFew = 8;
+template <int L, int C>
+__device__ __forceinline__ bool take_few(const int32_t* key, int k, int2* slots, int32_t* chosen, float* logits) {
+    const int lane = threadIdx.x & 63, l = lane % L, place = lane & 15;
+    int32_t m = key[0];
+#pragma unroll
+    for (int c = 1; c < C; ++c) m = max(m, key[c]);
+    auto larger = [](int32_t a, int32_t b) { return max(a, b); };
+    if constexpr (L > 16) m = team_step<16>(m, larger);
+    if constexpr (L > 32) m = team_step<32>(m, larger);
+    int before = 0;
+    row_turns([&](auto r) { before += (int32_t)lane_move<0x120 + r.value>((uint32_t)m) > m; });
+    const int32_t bound = max(kLowest + 1, team_reduce<16>(before < k ? m : INT32_MAX,
+                                                           [](int32_t a, int32_t b) { return min(a, b); }));
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < C; ++c) n += key[c] >= bound;
+    // their places, in the order of the experts
+    int upto = row_prefix(n), all = __builtin_amdgcn_ds_bpermute((lane | 15) << 2, upto);
+    if constexpr (L > 16) {
+        const int whole = wave_prefix(n);
+        const int first = L == 64 ? 0 : __builtin_amdgcn_ds_bpermute(((lane & -L) - 1) << 2, whole);
+        upto = whole - (lane < L ? 0 : first);
+        all = __builtin_amdgcn_ds_bpermute((lane | (L - 1)) << 2, upto);
+    }
+    if (__ballot(all > 16)) return false;
+    int at = upto - n;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+        if (key[c] >= bound) slots[at++] = make_int2(key[c], l * C + c);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    const int2 mine = place < all ? slots[place] : make_int2(kTaken, 0);
+    before = 0;
+    row_turns([&](auto r) {
+        // lane p sees lane p - r: with p >= r an expert before its own
+        const int32_t other = (int32_t)lane_move<0x120 + r.value>((uint32_t)mine.x);
+        before += other > (place >= r.value ? mine.x - 1 : mine.x);
+    });
+    if (l < 16 && place < all && before < k) {
+        chosen[before] = mine.y;
+        logits[before] = logit_of(mine.x);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    return true;
+}
+
 // The exclusive prefix sums of n <= 1024 counts, and their sum at [n].
 __device__ __forceinline__ void prefix_counts(int32_t* s, int n, int32_t* wave_sum) {
     constexpr int Q = kRouterMaxExperts / kThreads;  // counts of a thread
@@ -132,12 +197,7 @@ __device__ __forceinline__ void prefix_counts(int32_t* s, int n, int32_t* wave_s
         v[q] = i < n ? s[i] : 0;
         sum += v[q];
     }
-    int upto = sum;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int up = __shfl_up(upto, off, 64);
-        if ((threadIdx.x & 63) >= off) upto += up;
-    }
+    const int upto = wave_prefix(sum);
     if ((threadIdx.x & 63) == 63) wave_sum[threadIdx.x >> 6] = upto;
     __syncthreads();  // every count is read, every wave's sum is there
     int at = upto - sum;
@@ -152,10 +212,9 @@ __device__ __forceinline__ void prefix_counts(int32_t* s, int n, int32_t* wave_s
     __syncthreads();
 }
 
-// Both losses, by one workgroup: thread t's terms, added over the workgroup.
+// The workgroup's sum in every thread.
 __device__ __forceinline__ double add_up(double v, double* red) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+    v = wave_sum64(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -190,6 +249,8 @@ struct RouterLds {
     float* probs;              // [waves][experts]
     int32_t* chosen;           // [64 * top_k]
     float* gates;              // [64 * top_k]
+    float* lse;                // [64]
+    int32_t* live;             // [64]
     __device__ __forceinline__ RouterLds(char* p, int experts, int top_k) {
         const int even = (experts + 1) & ~1;
         mask = reinterpret_cast<unsigned long long*>(p);
@@ -197,11 +258,13 @@ struct RouterLds {
         probs = reinterpret_cast<float*>(first + even + 2);
         chosen = reinterpret_cast<int32_t*>(probs + kWaves * even);
         gates = reinterpret_cast<float*>(chosen + kRouterTokens * top_k);
+        lse = gates + kRouterTokens * top_k;
+        live = reinterpret_cast<int32_t*>(lse + kRouterTokens);
     }
 };
 size_t router_lds(int experts, int top_k) {
     const size_t even = ((size_t)experts + 1) & ~(size_t)1;
-    return (size_t)experts * 8 + (even + 2) * 4 + kWaves * even * 4 + (size_t)kRouterTokens * top_k * 8;
+    return (size_t)experts * 8 + (even + 2) * 4 + kWaves * even * 4 + (size_t)kRouterTokens * (top_k + 1) * 8;
 }
 
 __device__ __forceinline__ void put_losses(const RouterCall& c, double balance, int64_t choices, double lse2,
@@ -221,18 +284,21 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
     __shared__ double red[kWaves];
     __shared__ int32_t wave_sum[kWaves];
     constexpr int TEAMS = 64 / L;  // of a wave
+    __shared__ int2 slots[L >= 16 ? kWaves * TEAMS : 1][16];
     const RouterLds m(lds, c.experts, c.top_k);
     const int lane = threadIdx.x & 63, l = lane % L, team = lane / L, wave = threadIdx.x >> 6;
     const int token0 = blockIdx.x * kRouterTokens, tokens = min(kRouterTokens, c.tokens - token0);
     for (int e = threadIdx.x; e < c.experts; e += kThreads) m.mask[e] = 0;
     for (int i = threadIdx.x; i < tokens * c.top_k; i += kThreads) m.chosen[i] = -1;
+    if (threadIdx.x < kRouterTokens) {
+        m.lse[threadIdx.x] = 0.f;
+        m.live[threadIdx.x] = 0;
+    }
     __syncthreads();
 
     float probs[C];
 #pragma unroll
     for (int i = 0; i < C; ++i) probs[i] = 0.f;
-    double lse2 = 0.0;
-    int live = 0;
     for (int first = wave * TEAMS; first < tokens; first += kWaves * TEAMS) {
         const int t = first + team;
         const bool has = t < tokens;
@@ -243,15 +309,21 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
 #pragma unroll
         for (int i = 0; i < C; ++i) probs[i] = fmaf(e[i], inv, probs[i]);
         if (l == 0 && x.live) {
-            const double lse = (double)x.top + (double)logf(x.total);
-            lse2 = fma(lse, lse, lse2);
-            ++live;
+            m.lse[t] = x.top + logf(x.total);
+            m.live[t] = 1;
         }
         // one choice after the other, by the lane that holds it
         int32_t key[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) key[i] = key_of(z[i]);
-        for (int j = 0; j < c.top_k; ++j) {
+        if (__ballot(x.total != x.total))  // a NaN somewhere: its key could be any
+#pragma unroll
+            for (int i = 0; i < C; ++i) key[i] = z[i] == z[i] ? key[i] : kTaken;
+        bool done = false;
+        if constexpr (L >= 16)
+            if (c.top_k <= kFew)
+                done = take_few<L, C>(key, c.top_k, slots[wave * TEAMS + team], m.chosen + t * c.top_k, m.gates + t * c.top_k);
+        for (int j = 0; j < (done ? 0 : c.top_k); ++j) {
             int32_t top;
             const int i = take<L, C>(key, top);
             if (i >= 0) {
@@ -265,7 +337,7 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
         for (int j = l; j < c.top_k; j += L) {
             if (!has) continue;
             float& g = m.gates[t * c.top_k + j];
-            g = m.chosen[t * c.top_k + j] >= 0 ? expf(g - x.top) : 0.f;
+            g = m.chosen[t * c.top_k + j] >= 0 ? exp_of(g - x.top) : 0.f;
             sum += g;
         }
         if (c.renormalize) sum = team_sum<L>(sum);
@@ -277,16 +349,13 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
     }
     // the teams of a wave have the same experts in the same lanes
 #pragma unroll
-    for (int off = L; off < 64; off <<= 1)
-#pragma unroll
-        for (int i = 0; i < C; ++i) probs[i] += __shfl_xor(probs[i], off, 64);
+    for (int i = 0; i < C; ++i) probs[i] = across_teams<L>(probs[i]);
     const int even = (c.experts + 1) & ~1;
     if (team == 0)
 #pragma unroll
         for (int i = 0; i < C; ++i)
             if (l * C + i < c.experts) m.probs[wave * even + l * C + i] = probs[i];
-    lse2 = add_up(lse2, red);
-    const int32_t alive = (int32_t)add_up((double)live, red);  // (both pass barriers: LDS is whole)
+    __syncthreads();
 
     const int64_t at = (int64_t)token0 * c.top_k;
     for (int i = threadIdx.x; i < tokens * c.top_k; i += kThreads) {
@@ -294,6 +363,18 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
         if (e >= 0) atomicOr(m.mask + e, 1ull << ((uint32_t)i / (uint32_t)c.top_k));
         gst(c.chosen + at + i, e);
         gst(c.gates + at + i, m.gates[i]);
+    }
+    // the last wave: every token's logarithm (kRouterTokens are a wave's lanes)
+    double lse2 = 0.0;
+    int32_t alive = 0;
+    if (wave == kWaves - 1) {
+        const double lse = m.lse[lane];
+        lse2 = wave_sum64(lse * lse);
+        alive = __popcll(__ballot(m.live[lane] != 0));
+        if (!ONE && lane == 0) {
+            gst(s.lse + blockIdx.x, lse2);
+            gst(s.live + blockIdx.x, alive);
+        }
     }
     __syncthreads();
     double balance = 0.0;
@@ -311,19 +392,13 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
             gst(s.probs + (int64_t)blockIdx.x * c.experts + e, p);
         }
     }
-    if (!ONE) {
-        if (threadIdx.x == 0) {
-            gst(s.lse + blockIdx.x, lse2);
-            gst(s.live + blockIdx.x, alive);
-        }
-        return;
-    }
+    if (!ONE) return;
     balance = add_up(balance, red);  // (and every count is in LDS)
     prefix_counts(m.first, c.experts, wave_sum);
     const int32_t all = m.first[c.experts];
     for (int e = threadIdx.x; e <= c.experts; e += kThreads) gst(c.offsets + e, m.first[e]);
     if (c.rows || c.order) put_rows(c, m.mask, m.first, all, token0, tokens, m.chosen);
-    if (threadIdx.x == 0) put_losses(c, balance, all, lse2, alive);
+    if (threadIdx.x == kThreads - 1) put_losses(c, balance, all, lse2, alive);
 }
 
 // Per expert: the workgroups' choices before each workgroup, and the sums over
@@ -350,16 +425,9 @@ __global__ __launch_bounds__(1024) void router_join_kernel(RouterCall c, RouterS
     {  // a wave an expert
         const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, mine = blockIdx.x * kJoinExperts + w;
         const int own = count[w][lane];
-        int upto = own;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int up = __shfl_up(upto, off, 64);
-            if (lane >= off) upto += up;
-        }
+        const int upto = wave_prefix(own);
         count[w][lane] = upto - own;
-        double q = prob[w][lane];
-#pragma unroll
-        for (int off = 32; off > 0; off >>= 1) q += __shfl_xor(q, off, 64);
+        const double q = wave_sum64(prob[w][lane]);
         if (lane == 63 && mine < c.experts) {
             gst(c.counts + mine, upto);
             gst(s.total + mine, q);
@@ -468,7 +536,7 @@ __global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradCall c)
                 for (int j = 0; j < c.top_k; ++j) {
                     const int e = gld(chosen + j);
                     if (!is(e)) continue;
-                    const float w = expf(logit(e) - top);
+                    const float w = exp_of(logit(e) - top);
                     sum += w;
                     dot = fmaf(w, gld(d + j), dot);
                 }
@@ -478,7 +546,7 @@ __global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradCall c)
                 const int e = gld(chosen + j);
                 if (!is(e)) continue;
                 const float v = gld(d + j);
-                const float w = c.renormalize ? expf(logit(e) - top) / sum * (v - dot) : v;
+                const float w = c.renormalize ? exp_of(logit(e) - top) / sum * (v - dot) : v;
 #pragma unroll
                 for (int i = 0; i < C; ++i)
                     if (l * C + i == e) (c.renormalize ? add[i] : g[i]) += w;
@@ -507,9 +575,9 @@ hipError_t with_team(int experts, F&& fn) {
     if (experts <= 16) return MUON_TEAM(2, 8);
     if (experts <= 32) return MUON_TEAM(4, 8);
     if (experts <= 64) return MUON_TEAM(8, 8);
-    if (experts <= 128) return MUON_TEAM(16, 8);
-    if (experts <= 256) return MUON_TEAM(32, 8);
-    if (experts <= 512) return MUON_TEAM(64, 8);
+    if (experts <= 128) return MUON_TEAM(8, 16);
+    if (experts <= 256) return MUON_TEAM(16, 16);
+    if (experts <= 512) return MUON_TEAM(32, 16);
     return MUON_TEAM(64, 16);
 #undef MUON_TEAM
 }
