@@ -26,6 +26,7 @@ struct NormCall {
     float* rstd;
     int32_t rows, heads, cols;
     int32_t bf16, weight_bf16, center;
+    int32_t nontemporal;  // set by the launch
     float eps;
     // gradient only
     void* dweight;  // null: not wanted

@@ -9,10 +9,17 @@
 //
 // Both directions are bound by HBM: the forward pass reads x and writes y, the
 // gradient reads x and dy and writes dx, each once.  A row stays in the
-// registers of its team of 8 to 512 lanes from its load to its store, so the
+// registers of its team of 8 to 1024 lanes from its load to its store, so the
 // variance is the mean of the squared differences themselves, in a second sum
-// over registers.  Weight and bias are read once per workgroup, which then
-// walks over rows.
+// over registers.  Workgroups walk over rows; weight and bias are read once each.
+//
+// A team of a wave or more reads its next row while it works on one.  That needs
+// loads and stores without a branch around them: where one may be left out, the
+// compiler waits for every access in flight instead of the loads it needs.  So
+// rows are read and written through buffer resources of their own length: what
+// lies behind a row reads as zero and is not written, a row that is not there
+// has no length, and the last unit of a row whose length is no multiple of a
+// unit starts earlier (its first elements are its neighbour's, computed twice).
 #include <type_traits>
 
 #include "block.h"
@@ -23,86 +30,189 @@ namespace muon {
 
 namespace {
 
-template <int L>
-constexpr int threads_of() { return L > 256 ? L : 256; }
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// V elements of weight or bias, `left` of them there; `absent` without one.
-template <int V>
-__device__ __forceinline__ void load_weight(const void* w, bool bf, int off, int left, float absent, float* out) {
+// Rows of large tensors, read once, are not kept in the caches, which are left to
+// what the call writes and the next one reads.  With other inputs in every call:
+// gradients of 128 MB tensors 81 -> 70 us, of 192 MB 116 -> 98, of 256 MB 151 ->
+// 126, with a reader of dx behind them 128 -> 107, 184 -> 161 and 239 -> 227 us;
+// tensors of 16 to 64 MB took the same time either way, and a call on the same 34
+// MB again and again 13 us instead of 16.  (Stores around the caches: forward
+// passes over the same 470 MB in every call 90 -> 72 us, but a reader of y behind
+// one loses more.)
+constexpr int kNontemporal = 2;
+constexpr int64_t kNontemporalBytes = (int64_t)96 << 20;  // of x
+
+// `bytes` bytes from p on, the same in every lane of the wave.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_resource(const void* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+}
+
+// V elements of weight or bias from column `at` on; `absent` without one.  Columns
+// behind the last read as anything.
+template <int V, bool WHOLE>
+__device__ __forceinline__ void load_weight(const void* w, bool bf, int at, int cols, float absent, float* out) {
     if (!w) {
 #pragma unroll
         for (int e = 0; e < V; ++e) out[e] = absent;
+    } else if (!WHOLE) {
+        // a last unit that is cut short
+        for (int e = 0; e < V; ++e) {
+            const int k = min(at + e, cols - 1);
+            out[e] = bf ? bf16_bits_to_f32(gld(reinterpret_cast<const uint16_t*>(w) + k))
+                        : gld(reinterpret_cast<const float*>(w) + k);
+        }
     } else if (bf) {
-        const Raw<true, V> r = load_raw<true, V, false>(w, off, left);
+        const auto r = row_resource(w, cols * 2);
+        if constexpr (V == 8) {
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, at * 2, 0, 0);
 #pragma unroll
-        for (int e = 0; e < V; ++e) out[e] = r.at(e);
+            for (int e = 0; e < 8; ++e) out[e] = bf16_bits_to_f32((uint16_t)(v[e / 2] >> 16 * (e & 1)));
+        } else {
+            const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(r, at * 2, 0, 0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[e] = bf16_bits_to_f32((uint16_t)(v[e / 2] >> 16 * (e & 1)));
+        }
     } else {
+        const auto r = row_resource(w, cols * 4);
 #pragma unroll
         for (int p = 0; p < V; p += 4) {
-            const Raw<false, 4> r = load_raw<false, 4, false>(w, off + p, left - p);
+            const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, (at + p) * 4, 0, 0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) out[p + e] = r.at(e);
+            for (int e = 0; e < 4; ++e) out[p + e] = __builtin_bit_cast(float, (uint32_t)v[e]);
         }
     }
 }
 
-// A team's row: lane l holds units l, l + L, ... of V elements.
+// Which elements of a row a lane of a team of L has: R units of V.  Unit i starts
+// at column at[i]; its first skip[i] elements are another unit's too (V: all are,
+// or there is no such unit).  EVEN: rows are whole units, nothing is skipped, and
+// at[i] >= cols where there is none.
 template <bool BF, bool EVEN, int L, int R>
-struct Row {
+struct Share {
     static constexpr int V = BF ? 8 : 4;
-    Raw<BF, V> u[R];
-    __device__ __forceinline__ void load(const void* base, int64_t off, int cols, int l, bool has) {
+    static constexpr int kNowhere = 1 << 24;  // behind every row
+    int at[R], skip[R];
+    __device__ __forceinline__ Share(int l, int cols) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int c = (i * L + l) * V, left = has ? cols - c : 0;
-            if (!EVEN) {
-                u[i] = load_raw<BF, V, false>(base, off + c, left);
-            } else if (left > 0) {
-                u[i] = load_raw<BF, V, true>(base, off + c, V);
-            } else {
-#pragma unroll
-                for (int k = 0; k < Raw<BF, V>::W; ++k) u[i].w[k] = 0;
+            const int c = (i * L + l) * V;
+            at[i] = c;
+            skip[i] = 0;
+            if (!EVEN && L >= 64 && c + V > cols) {
+                at[i] = c < cols ? cols - V : kNowhere;
+                skip[i] = c < cols ? c - (cols - V) : V;
             }
+        }
+    }
+    // whether element e of unit i is in the row, and this lane's to count
+    __device__ __forceinline__ bool mine(int i, int e, int cols) const {
+        if (EVEN) return at[i] < cols;
+        return L >= 64 ? e >= skip[i] : at[i] + e < cols;
+    }
+    // a unit that a row of a team of this size may not have (those of the second
+    // half of L * R: smaller teams take rows without them)
+    static constexpr bool maybe(int i) { return R == 1 || 2 * i >= R; }
+};
+
+// A row, as it is in memory.
+template <bool BF, bool EVEN, int L, int R>
+struct Row {
+    static constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4;
+    Raw<BF, V> u[R];
+    template <bool NT>
+    __device__ __forceinline__ void read(const void* base, int64_t off, int cols, const Share<BF, EVEN, L, R>& s, bool has) {
+        if constexpr (L >= 64) {
+            const auto r = row_resource(reinterpret_cast<const char*>(base) + off * ES, has ? cols * ES : 0);
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(r, s.at[i] * ES, 0, NT ? kNontemporal : 0);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) u[i].w[k] = v[k];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < R; ++i) {
+                const int left = has ? cols - s.at[i] : 0;
+                if (!EVEN) {
+                    u[i] = load_raw<BF, V, false, NT>(base, off + s.at[i], left);
+                } else {
+                    // from the row's start where there is no such unit
+                    u[i] = load_raw<BF, V, true, NT>(base, off + (left > 0 ? s.at[i] : 0), V);
+#pragma unroll
+                    for (int k = 0; k < Raw<BF, V>::W; ++k) u[i].w[k] = left > 0 ? u[i].w[k] : 0;
+                }
+            }
+        }
+    }
+    // NT: around the caches; for teams of a wave or more `nontemporal` says so (a
+    // branch there, not a kernel: the aux bits of the two loads keep the compiler
+    // from making one of them).
+    template <bool NT>
+    __device__ __forceinline__ void load(const void* base, int64_t off, int cols, const Share<BF, EVEN, L, R>& s, bool has,
+                                         bool nontemporal) {
+        if (NT || (L >= 64 && nontemporal))
+            read<true>(base, off, cols, s, has);
+        else
+            read<false>(base, off, cols, s, has);
+    }
+};
+
+// Writes v, unit i of a row at a time.
+template <bool BF, bool EVEN, int L, int R>
+struct Out {
+    static constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4;
+    char* p;
+    int cols;
+    bool has;
+    __device__ __forceinline__ Out(void* base, int64_t off, int cols_, bool has_)
+        : p(reinterpret_cast<char*>(base) + off * ES), cols(cols_), has(has_) {}
+    __device__ __forceinline__ void put(int i, const Share<BF, EVEN, L, R>& s, const float* v) const {
+        if constexpr (L >= 64) {
+            u32x4 w;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = BF ? (uint32_t)f32_to_bf16_bits(v[2 * k]) | (uint32_t)f32_to_bf16_bits(v[2 * k + 1]) << 16
+                          : __builtin_bit_cast(uint32_t, v[k]);
+            __builtin_amdgcn_raw_buffer_store_b128(w, row_resource(p, has ? cols * ES : 0), s.at[i] * ES, 0, 0);
+        } else if (has) {
+            const int left = cols - s.at[i];
+            if (!EVEN)
+                store_unit<V, BF, false>(p, s.at[i], left, v);
+            else if (left > 0)
+                store_unit<V, BF, true>(p, s.at[i], V, v);
         }
     }
 };
 
-template <bool BF, bool EVEN>
-__device__ __forceinline__ void store_row(void* base, int64_t off, int left, const float* v) {
-    constexpr int V = BF ? 8 : 4;
-    if (!EVEN)
-        store_unit<V, BF, false>(base, off, left, v);
-    else if (left > 0)
-        store_unit<V, BF, true>(base, off, V, v);
-}
-
-// Sums over a team.  A team of more lanes than a wave has is a whole
-// workgroup: its waves meet in LDS, in one of two slots in turn, so that one
-// barrier a sum is enough (a wave that writes a slot again has passed the
-// other slot's barrier, which every wave reaches after it has read).
-template <int L>
+// Sums over a team.  The waves of a team of more lanes than a wave has meet in
+// LDS, in one of two slots in turn, so that one barrier a sum is enough (a wave
+// that writes a slot again has passed the other slot's barrier, which every wave
+// reaches after it has read).  NT: threads of the workgroup.
+template <int L, int NT>
 struct TeamSum {
     float* red;  // [2][2 * waves]
     int slot = 0;
     __device__ __forceinline__ explicit TeamSum(float* r) : red(r) {}
     __device__ __forceinline__ void operator()(float& a, float& b, bool two) {
-        constexpr int W = L > 64 ? L / 64 : 1;
+        constexpr int W = L > 64 ? L / 64 : 1, ALL = NT / 64;
         a = team_sum<(L > 64 ? 64 : L)>(a);
         if (two) b = team_sum<(L > 64 ? 64 : L)>(b);
         if constexpr (W > 1) {
-            float* s = red + slot * 2 * W;
-            const int w = threadIdx.x >> 6;
+            float* s = red + slot * 2 * ALL;
+            const int w = threadIdx.x >> 6, w0 = w / W * W;
             if ((threadIdx.x & 63) == 0) {
                 s[w] = a;
-                s[W + w] = b;
+                s[ALL + w] = b;
             }
             __syncthreads();
-            a = s[0];
-            b = s[W];
+            a = s[w0];
+            b = s[ALL + w0];
 #pragma unroll
             for (int i = 1; i < W; ++i) {
-                a += s[i];
-                b += s[W + i];
+                a += s[w0 + i];
+                b += s[ALL + w0 + i];
             }
             slot ^= 1;
         }
@@ -115,25 +225,65 @@ __device__ __forceinline__ int64_t row_at(int row, int heads, int64_t token, int
     return t * token + (row - (int)t * heads) * head;
 }
 
-template <bool BF, bool EVEN, int L, int R>
+// The team of a thread; one of a wave or more is the same in all its lanes.
+template <int L>
+__device__ __forceinline__ int team_of() {
+    const int t = threadIdx.x / L;
+    return L >= 64 ? __builtin_amdgcn_readfirstlane(t) : t;
+}
+
+// Calls work(row buffer, first row of the workgroup's teams) for the rows first,
+// first + stride, ...; with AHEAD, load(buffer, first) has read the next ones by
+// then.
+template <class B, bool AHEAD, class Load, class Work>
+__device__ __forceinline__ void walk_rows(int64_t first, int64_t stride, int rows, Load&& load, Work&& work) {
+    B a, b;
+    if constexpr (!AHEAD) {
+        for (; first < rows; first += stride) {
+            load(a, first);
+            work(a, first);
+        }
+        return;
+    }
+    load(a, first);
+    while (true) {
+        load(b, first + stride);
+        work(a, first);
+        first += stride;
+        if (first >= rows) return;
+        load(a, first + stride);
+        work(b, first);
+        first += stride;
+        if (first >= rows) return;
+    }
+}
+
+template <int L>
+constexpr int threads_of() { return L > 256 ? L : 256; }
+
+template <bool BF, bool EVEN, int L, int R, bool NT>
 __global__ __launch_bounds__(threads_of<L>()) void norm_forward_kernel(NormCall c) {
-    constexpr int V = BF ? 8 : 4, TEAMS = threads_of<L>() / L;
-    __shared__ float red[L > 64 ? 4 * (L / 64) : 1];
-    const int l = threadIdx.x % L, team = threadIdx.x / L;
+    constexpr int V = BF ? 8 : 4, THREADS = threads_of<L>(), TEAMS = THREADS / L;
+    __shared__ float red[L > 64 ? 4 * (THREADS / 64) : 1];
+    const int l = threadIdx.x % L, team = team_of<L>();
+    const Share<BF, EVEN, L, R> s(l, c.cols);
     float w[R][V], b[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int col = (i * L + l) * V;
-        load_weight<V>(c.weight, c.weight_bf16, col, c.cols - col, 1.f, w[i]);
-        load_weight<V>(c.bias, c.weight_bf16, col, c.cols - col, 0.f, b[i]);
+        load_weight<V, EVEN || L >= 64>(c.weight, c.weight_bf16, s.at[i], c.cols, 1.f, w[i]);
+        load_weight<V, EVEN || L >= 64>(c.bias, c.weight_bf16, s.at[i], c.cols, 0.f, b[i]);
     }
-    TeamSum<L> sum(red);
+    TeamSum<L, THREADS> sum(red);
     const float n = (float)c.cols;
-    for (int64_t first = (int64_t)blockIdx.x * TEAMS; first < c.rows; first += (int64_t)gridDim.x * TEAMS) {
+    using Buffer = Row<BF, EVEN, L, R>;
+    auto load = [&](Buffer& x, int64_t first) {
+        const int64_t row = first + team;
+        const bool has = row < c.rows;
+        x.template load<NT>(c.x, row_at(has ? (int)row : 0, c.heads, c.x_token, c.x_head), c.cols, s, has, c.nontemporal);
+    };
+    auto work = [&](const Buffer& x, int64_t first) {
         const int row = (int)first + team;
         const bool has = row < c.rows;
-        Row<BF, EVEN, L, R> x;
-        x.load(c.x, has ? row_at(row, c.heads, c.x_token, c.x_head) : 0, c.cols, l, has);
         float v[R][V], mean = 0.f, none = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i)
@@ -143,38 +293,37 @@ __global__ __launch_bounds__(threads_of<L>()) void norm_forward_kernel(NormCall 
 #pragma unroll
             for (int i = 0; i < R; ++i)
 #pragma unroll
-                for (int e = 0; e < V; ++e) mean += v[i][e];
+                for (int e = 0; e < V; ++e)
+                    // (what is behind the row reads as zero)
+                    mean += !EVEN && L >= 64 && s.maybe(i) && !s.mine(i, e, c.cols) ? 0.f : v[i][e];
             sum(mean, none, false);
             mean /= n;
         }
         float sq = 0.f;
 #pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int left = c.cols - (i * L + l) * V;
+        for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 v[i][e] -= mean;
-                // places behind the row are not part of its variance
-                const float d = (EVEN ? left > 0 : e < left) ? v[i][e] : 0.f;
+                const float d = !s.maybe(i) || s.mine(i, e, c.cols) ? v[i][e] : 0.f;
                 sq = fmaf(d, d, sq);
             }
-        }
         sum(sq, none, false);
         const float rstd = 1.f / sqrtf(sq / n + c.eps);
-        if (!has) continue;
-        if (l == 0) {
+        const Out<BF, EVEN, L, R> out(c.out, has ? row_at(row, c.heads, c.out_token, c.out_head) : 0, c.cols, has);
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            float o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = fmaf(v[i][e] * rstd, w[i][e], b[i][e]);
+            out.put(i, s, o);
+        }
+        if (l == 0 && has) {
             if (c.mean) gst(c.mean + row, mean);
             if (c.rstd) gst(c.rstd + row, rstd);
         }
-        const int64_t at = row_at(row, c.heads, c.out_token, c.out_head);
-#pragma unroll
-        for (int i = 0; i < R; ++i) {
-            const int col = (i * L + l) * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] = fmaf(v[i][e] * rstd, w[i][e], b[i][e]);
-            store_row<BF, EVEN>(c.out, at + col, c.cols - col, v[i]);
-        }
-    }
+    };
+    walk_rows<Buffer, L >= 64>((int64_t)blockIdx.x * TEAMS, (int64_t)gridDim.x * TEAMS, c.rows, load, work);
 }
 
 __device__ __forceinline__ void put_grad(void* p, bool bf, int accumulate, int col, double v) {
@@ -189,90 +338,126 @@ __device__ __forceinline__ void put_grad(void* p, bool bf, int accumulate, int c
     }
 }
 
-// dx, and each workgroup's sums for dw and db over its rows.
-template <bool BF, bool EVEN, int L, int R>
-__global__ __launch_bounds__(threads_of<L>()) void norm_grad_kernel(NormCall c) {
-    constexpr int V = BF ? 8 : 4, NT = threads_of<L>(), TEAMS = NT / L;
-    __shared__ float red[L > 64 ? 4 * (L / 64) : NT * R * V];
-    const int l = threadIdx.x % L, team = threadIdx.x / L;
-    float w[R][V], dw[R][V], db[R][V];
+// Threads of the gradient's workgroups: 256, or two teams that are wider than a
+// wave.  Each team adds its rows to sums of its own, and the workgroup hands on
+// one sum a column: fewer, wider workgroups leave less to join.
+// (A lane's fp32 rows take twice the registers: 128, which 1024 threads have, are
+// not enough for two teams of 512.)
+template <bool BF, int L>
+constexpr int grad_threads() { return L > 512 || (BF && L > 256) ? 1024 : L > 64 ? 512 : 256; }
+
+// dx, and each workgroup's sums for dw and db over its rows.  The weight of a row
+// of more than a wave is kept in LDS, which leaves those registers to the next row.
+template <bool BF, bool EVEN, int L, int R, bool NT>
+__global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(NormCall c) {
+    constexpr int V = BF ? 8 : 4, THREADS = grad_threads<BF, L>(), TEAMS = THREADS / L;
+    constexpr bool WIDE = L > 64;
+    __shared__ float red[WIDE ? 4 * (THREADS / 64) : 1];
+    // the weight, then the teams' sums
+    __shared__ __align__(16) float held[WIDE ? L * R * V : THREADS * R * V];
+    const int l = threadIdx.x % L, team = team_of<L>();
+    const Share<BF, EVEN, L, R> s(l, c.cols);
+    // (a wide row's values: 16 bytes of a lane beside those of the next)
+    auto held_at = [&](int i, int e) { return ((i * (V / 4) + e / 4) * L + l) * 4 + e % 4; };
+    float w[WIDE ? 1 : R][V], dw[R][V], db[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        const int col = (i * L + l) * V;
-        load_weight<V>(c.weight, c.weight_bf16, col, c.cols - col, 1.f, w[i]);
+        float v[V];
+        load_weight<V, EVEN || L >= 64>(c.weight, c.weight_bf16, s.at[i], c.cols, 1.f, v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.f;
+        for (int e = 0; e < V; ++e) {
+            if (!WIDE)
+                w[i][e] = v[e];
+            else if (team == 0)
+                held[held_at(i, e)] = v[e];
+            dw[i][e] = db[i][e] = 0.f;
+        }
     }
-    TeamSum<L> sum(red);
+    if (WIDE) __syncthreads();
+    TeamSum<L, THREADS> sum(red);
     const float n = (float)c.cols;
-    for (int64_t first = (int64_t)blockIdx.x * TEAMS; first < c.rows; first += (int64_t)gridDim.x * TEAMS) {
+    struct Buffer {
+        Row<BF, EVEN, L, R> x, dy;
+        float mean, rstd;
+    };
+    auto load = [&](Buffer& r, int64_t first) {
+        const int64_t row = first + team;
+        const bool has = row < c.rows;
+        const int there = has ? (int)row : 0;
+        r.x.template load<NT>(c.x, row_at(there, c.heads, c.x_token, c.x_head), c.cols, s, has, c.nontemporal);
+        r.dy.template load<NT>(c.dy, row_at(there, c.heads, c.dy_token, c.dy_head), c.cols, s, has, c.nontemporal);
+        r.mean = c.center ? gld(c.mean + there) : 0.f;
+        r.rstd = gld(c.rstd + there);
+    };
+    auto work = [&](const Buffer& r, int64_t first) {
         const int row = (int)first + team;
         const bool has = row < c.rows;
-        Row<BF, EVEN, L, R> x, dy;
-        x.load(c.x, has ? row_at(row, c.heads, c.x_token, c.x_head) : 0, c.cols, l, has);
-        dy.load(c.dy, has ? row_at(row, c.heads, c.dy_token, c.dy_head) : 0, c.cols, l, has);
-        const float mean = has && c.center ? gld(c.mean + row) : 0.f, rstd = has ? gld(c.rstd + row) : 0.f;
+        const float mu = has ? r.mean : 0.f, rs = has ? r.rstd : 0.f;
+        auto weight = [&](int i, int e) { return WIDE ? held[held_at(i, e)] : w[WIDE ? 0 : i][e]; };
         float s1 = 0.f, s2 = 0.f;
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const float hat = (x.u[i].at(e) - mean) * rstd, d = dy.u[i].at(e), g = d * w[i][e];
-                dw[i][e] = fmaf(d, hat, dw[i][e]);
+                float d = r.dy.u[i].at(e);
+                if (!EVEN && L >= 64 && s.maybe(i)) d = s.mine(i, e, c.cols) ? d : 0.f;
+                const float t = r.x.u[i].at(e) - mu, g = d * weight(i, e);
+                dw[i][e] = fmaf(d * rs, t, dw[i][e]);
                 db[i][e] += d;
-                s1 = fmaf(g, hat, s1);
+                s1 = fmaf(g, t, s1);
                 s2 += g;
             }
-        if (!c.out) continue;
+        if (!c.out) return;
         sum(s1, s2, c.center);
-        s1 /= n;
-        s2 = c.center ? s2 / n : 0.f;
-        if (!has) continue;
-        const int64_t at = row_at(row, c.heads, c.out_token, c.out_head);
+        // dx = rstd g - rstd^3 (x - mean) sum(g (x - mean)) / C - rstd sum(g) / C
+        const float a = -(s1 * rs / n) * rs * rs, b = c.center ? -(s2 / n) * rs : 0.f;
+        const Out<BF, EVEN, L, R> out(c.out, has ? row_at(row, c.heads, c.out_token, c.out_head) : 0, c.cols, has);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
-            const int col = (i * L + l) * V;
             float o[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                const float hat = (x.u[i].at(e) - mean) * rstd, g = dy.u[i].at(e) * w[i][e];
-                o[e] = rstd * (g - s2 - hat * s1);
-            }
-            store_row<BF, EVEN>(c.out, at + col, c.cols - col, o);
+            for (int e = 0; e < V; ++e)
+                o[e] = fmaf(r.dy.u[i].at(e) * weight(i, e), rs, fmaf(r.x.u[i].at(e) - mu, a, b));
+            out.put(i, s, o);
         }
-    }
+    };
+    // (1024 threads have 128 registers each: no room for two rows)
+    walk_rows<Buffer, L <= 512>((int64_t)blockIdx.x * TEAMS, (int64_t)gridDim.x * TEAMS, c.rows, load, work);
     // the teams' sums, added in their order
     auto put = [&](int side, float (&acc)[R][V], void* out) {
         if (!out) return;
+        float* p = c.partials + ((int64_t)side * gridDim.x + blockIdx.x) * c.cols;
         if constexpr (TEAMS > 1) {
+            auto place = [&](int t, int i, int e) { return WIDE ? held_at(i, e) : ((t * R + i) * V + e) * L + l; };
             __syncthreads();
+            if (!WIDE || team == 1)
 #pragma unroll
-            for (int i = 0; i < R; ++i)
+                for (int i = 0; i < R; ++i)
 #pragma unroll
-                for (int e = 0; e < V; ++e) red[(team * R + i) * L * V + l * V + e] = acc[i][e];
+                    for (int e = 0; e < V; ++e) held[place(team, i, e)] = acc[i][e];
             __syncthreads();
-            for (int col = threadIdx.x; col < c.cols; col += NT) {
-                float s = red[col];
-                for (int t = 1; t < TEAMS; ++t) s += red[t * R * L * V + col];
-                if (gridDim.x == 1)
-                    put_grad(out, c.grad_bf16, c.accumulate, col, s);
-                else
-                    gst(c.partials + ((int64_t)side * gridDim.x + blockIdx.x) * c.cols + col, s);
-            }
-        } else {
+            if (team == 0)
 #pragma unroll
-            for (int i = 0; i < R; ++i) {
-                const int col = (i * L + l) * V;
-                if (gridDim.x == 1) {
+                for (int i = 0; i < R; ++i)
 #pragma unroll
                     for (int e = 0; e < V; ++e)
-                        if (col + e < c.cols) put_grad(out, c.grad_bf16, c.accumulate, col + e, acc[i][e]);
-                } else {
-                    float* p = c.partials + ((int64_t)side * gridDim.x + blockIdx.x) * c.cols;
+                        for (int t = 1; t < TEAMS; ++t) acc[i][e] += held[place(t, i, e)];
+        }
+        if (team > 0) return;
 #pragma unroll
-                    for (int h = 0; h < V; h += 4)
-                        store_unit<4, false, false>(p, col + h, c.cols - col - h, &acc[i][h]);
-                }
+        for (int i = 0; i < R; ++i) {
+            if (gridDim.x > 1 && s.mine(i, 0, c.cols) && s.mine(i, V - 1, c.cols)) {
+#pragma unroll
+                for (int e = 0; e < V; e += 4) store_unit<4, false, true>(p, s.at[i] + e, 4, &acc[i][e]);
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                if (!s.mine(i, e, c.cols)) continue;
+                if (gridDim.x == 1)
+                    put_grad(out, c.grad_bf16, c.accumulate, s.at[i] + e, acc[i][e]);
+                else
+                    gst(p + s.at[i] + e, acc[i][e]);
             }
         }
     };
@@ -281,7 +466,7 @@ __global__ __launch_bounds__(threads_of<L>()) void norm_grad_kernel(NormCall c) 
 }
 
 // dw and db from the workgroups' sums: 64 columns a workgroup, each of its 16
-// waves every 16th sum, in 64 bits.
+// waves every 16th sum, eight of them in flight, added in 64 bits.
 __global__ __launch_bounds__(1024) void norm_grad_join_kernel(NormCall c, int blocks) {
     __shared__ double part[16][64];
     void* out = blockIdx.y ? c.dbias : c.dweight;
@@ -290,7 +475,15 @@ __global__ __launch_bounds__(1024) void norm_grad_join_kernel(NormCall c, int bl
     double s = 0.0;
     if (col < c.cols) {
         const float* p = c.partials + (int64_t)blockIdx.y * blocks * c.cols + col;
-        for (int b = wave; b < blocks; b += 16) s += gld(p + (int64_t)b * c.cols);
+        int b = wave;
+        for (; b + 7 * 16 < blocks; b += 8 * 16) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = gld(p + (int64_t)(b + 16 * i) * c.cols);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += v[i];
+        }
+        for (; b < blocks; b += 16) s += gld(p + (int64_t)b * c.cols);
     }
     part[wave][lane] = s;
     __syncthreads();
@@ -313,8 +506,33 @@ hipError_t with_team(int units, F&& fn) {
     if (units <= 256) return MUON_TEAM(256, 1);
     if (units <= 512) return MUON_TEAM(256, 2);
     if (units <= 1024) return MUON_TEAM(256, 4);
-    if (BF || units <= 2048) return MUON_TEAM(512, 4);
-    return MUON_TEAM(512, 8);
+    if constexpr (!BF)
+        if (units > 2048) return MUON_TEAM(512, 8);
+    return MUON_TEAM(512, 4);
+#undef MUON_TEAM
+}
+
+// The same for the gradient, whose sums for dw and db take two registers a value:
+// at most 16 values a lane.
+template <bool BF, class F>
+hipError_t with_grad_team(int units, F&& fn) {
+    using std::integral_constant;
+#define MUON_TEAM(L, R) fn(integral_constant<int, L>{}, integral_constant<int, R>{})
+    if (units <= 8) return MUON_TEAM(8, 1);
+    if (units <= 16) return MUON_TEAM(16, 1);
+    if (units <= 32) return MUON_TEAM(32, 1);
+    if (units <= 64) return MUON_TEAM(64, 1);
+    if (units <= 128) return MUON_TEAM(64, 2);
+    if (units <= 256) return MUON_TEAM(256, 1);
+    if (units <= 512) return MUON_TEAM(256, 2);
+    if constexpr (BF) {
+        if (units <= 1024) return MUON_TEAM(512, 2);
+        return MUON_TEAM(1024, 2);
+    } else {
+        if (units <= 1024) return MUON_TEAM(256, 4);
+        if (units <= 2048) return MUON_TEAM(512, 4);
+        return MUON_TEAM(1024, 4);
+    }
 #undef MUON_TEAM
 }
 
@@ -327,6 +545,11 @@ int blocks_for(int rows, int teams, int cus, int each) {
     return (int)(need < (int64_t)cus * each ? need : (int64_t)cus * each);
 }
 
+NormCall with_loads(NormCall c) {
+    c.nontemporal = (int64_t)c.rows * c.cols * (c.bf16 ? 2 : 4) >= kNontemporalBytes;
+    return c;
+}
+
 template <class F>
 hipError_t with_types(const NormCall& c, F&& fn) {
     const bool even = c.cols % (c.bf16 ? 8 : 4) == 0;
@@ -336,12 +559,16 @@ hipError_t with_types(const NormCall& c, F&& fn) {
 
 }  // namespace
 
-hipError_t launch_norm_forward(const NormCall& c, int cus, hipStream_t st) {
+hipError_t launch_norm_forward(const NormCall& call, int cus, hipStream_t st) {
+    const NormCall c = with_loads(call);
     return with_types(c, [&](auto bf, auto even) {
         return with_team<bf.value>(units_of(c.cols, c.bf16), [&](auto l, auto r) {
             constexpr int NT = threads_of<l.value>();
             const int blocks = blocks_for(c.rows, NT / l.value, cus, NT > 256 ? 2 : 8);
-            norm_forward_kernel<bf.value, even.value, l.value, r.value><<<blocks, NT, 0, st>>>(c);
+            if (l.value < 64 && c.nontemporal)
+                norm_forward_kernel<bf.value, even.value, l.value, r.value, l.value < 64><<<blocks, NT, 0, st>>>(c);
+            else
+                norm_forward_kernel<bf.value, even.value, l.value, r.value, false><<<blocks, NT, 0, st>>>(c);
             return hipGetLastError();
         });
     });
@@ -349,21 +576,29 @@ hipError_t launch_norm_forward(const NormCall& c, int cus, hipStream_t st) {
 
 int norm_grad_blocks(int32_t rows, int32_t cols, bool bf16, int cus) {
     int blocks = 0;
-    // (a unit's lanes do not depend on its type)
-    (void)with_team<false>(units_of(cols, bf16), [&](auto l, auto) {
-        constexpr int NT = threads_of<l.value>();
-        blocks = blocks_for(rows, NT / l.value, cus, NT > 256 ? 1 : 2);
+    auto count = [&](auto bf, auto l, auto r) {
+        constexpr int NT = grad_threads<bf.value, l.value>();
+        // as many as registers leave room for
+        blocks = blocks_for(rows, NT / l.value, cus, NT > 512 ? 1 : NT > 256 || r.value > 1 ? 2 : 4);
         return hipSuccess;
-    });
+    };
+    const int units = units_of(cols, bf16);
+    (void)(bf16 ? with_grad_team<true>(units, [&](auto l, auto r) { return count(std::true_type{}, l, r); })
+                : with_grad_team<false>(units, [&](auto l, auto r) { return count(std::false_type{}, l, r); }));
     return blocks;
 }
 
-hipError_t launch_norm_grad(const NormCall& c, int cus, hipStream_t st) {
+hipError_t launch_norm_grad(const NormCall& call, int cus, hipStream_t st) {
+    const NormCall c = with_loads(call);
     const int blocks = norm_grad_blocks(c.rows, c.cols, c.bf16, cus);
     hipError_t e = hipSuccess;
     if (blocks > 0) e = with_types(c, [&](auto bf, auto even) {
-        return with_team<bf.value>(units_of(c.cols, c.bf16), [&](auto l, auto r) {
-            norm_grad_kernel<bf.value, even.value, l.value, r.value><<<blocks, threads_of<l.value>(), 0, st>>>(c);
+        return with_grad_team<bf.value>(units_of(c.cols, c.bf16), [&](auto l, auto r) {
+            constexpr int NT = grad_threads<bf.value, l.value>();
+            if (l.value < 64 && c.nontemporal)
+                norm_grad_kernel<bf.value, even.value, l.value, r.value, l.value < 64><<<blocks, NT, 0, st>>>(c);
+            else
+                norm_grad_kernel<bf.value, even.value, l.value, r.value, false><<<blocks, NT, 0, st>>>(c);
             return hipGetLastError();
         });
     });

@@ -24,21 +24,25 @@ struct Raw {
 };
 
 // The V elements at offset `off`; `left`: elements the row still holds.  FULL:
-// at least V of them, known without looking.
-template <bool BF, int V, bool FULL>
+// at least V of them, known without looking.  NT: whole units are not kept in the
+// caches.
+template <bool BF, int V, bool FULL, bool NT = false>
 __device__ __forceinline__ Raw<BF, V> load_raw(const void* base, int64_t off, int64_t left) {
     Raw<BF, V> r;
     if (FULL || left >= V) {
         if constexpr (!BF) {
-            const u32x4u u = *(const MUON_GLOBAL u32x4u*)(reinterpret_cast<const float*>(base) + off);
+            const MUON_GLOBAL u32x4u* p = (const MUON_GLOBAL u32x4u*)(reinterpret_cast<const float*>(base) + off);
+            const u32x4u u = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
             for (int i = 0; i < 4; ++i) r.w[i] = u[i];
         } else if constexpr (V == 8) {
-            const u32x4h u = *(const MUON_GLOBAL u32x4h*)(reinterpret_cast<const uint16_t*>(base) + off);
+            const MUON_GLOBAL u32x4h* p = (const MUON_GLOBAL u32x4h*)(reinterpret_cast<const uint16_t*>(base) + off);
+            const u32x4h u = NT ? __builtin_nontemporal_load(p) : *p;
 #pragma unroll
             for (int i = 0; i < 4; ++i) r.w[i] = u[i];
         } else {
-            const u32x2h u = *(const MUON_GLOBAL u32x2h*)(reinterpret_cast<const uint16_t*>(base) + off);
+            const MUON_GLOBAL u32x2h* p = (const MUON_GLOBAL u32x2h*)(reinterpret_cast<const uint16_t*>(base) + off);
+            const u32x2h u = NT ? __builtin_nontemporal_load(p) : *p;
             r.w[0] = u[0];
             r.w[1] = u[1];
         }
