@@ -9,7 +9,9 @@
 //
 // Bound by HBM: every element is read and written once.  A workgroup takes a
 // run of tokens of one tensor and forms their sines and cosines once, for all
-// heads, in LDS.  Angles are formed in 64 bits and reduced to a part of a turn
+// heads, in LDS.  A thread has one unit of two 16-byte runs (two units a thread:
+// 124 us instead of 120 for 32768 tokens of 32 + 8 heads of 128 in bf16, four: 127;
+// without sines 123 with two).  Angles are formed in 64 bits and reduced to a part of a turn
 // there: an fp32 product of a position and a frequency is off by up to 2^-24 of
 // the angle, 0.06 radians at position 10^6.
 #include <type_traits>
@@ -21,8 +23,7 @@ namespace muon {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnits = 4;       // of a thread, all loaded before the first is used
+constexpr int kThreads = 512;  // 256: 142 us for the fp32 heads below instead of 137, the same for bf16
 constexpr int64_t kRotaryNontemporalBytes = (int64_t)96 << 20;
 constexpr int kTable = kRotaryPairs;  // (cosine, sine) of a workgroup's tokens, whole units of them
 
@@ -48,8 +49,8 @@ __device__ __forceinline__ int divided(int v, float inv) { return (int)(((float)
 
 // INTER: neighbours are pairs.  WHOLE: no unit is cut short; a unit's two runs of V
 // elements then lie half its part apart, so that the lanes of a load or store
-// follow each other (runs side by side: 190 us for 806 MB of fp32 heads with 128
-// elements copied and 32 pairs of neighbours).  NT: loads around the caches.
+// follow each other (806 MB of fp32 heads with 128 elements copied and 32 pairs of
+// neighbours 156 us, 190 with the runs side by side, two units a thread each).  NT: loads around the caches.
 template <bool BF, bool INTER, bool WHOLE, bool NT>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryCall c, RotaryPlaces places) {
     constexpr int V = BF ? 8 : 4;
@@ -57,7 +58,12 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryCall c, RotaryPl
     // units + i][b]: 16 bytes of a lane beside those of the lane with the next unit
     __shared__ __align__(16) float2 table[kTable];
     int block = blockIdx.x, which = 0;
-    while (block >= places.p[which].blocks) block -= places.p[which++].blocks;
+#pragma unroll
+    for (int i = 0; i + 1 < kRotaryTensors; ++i) {  // (a tensor that is not there has no workgroups)
+        const bool next = which == i && block >= places.p[i].blocks;
+        block -= next ? places.p[i].blocks : 0;
+        which += next;
+    }
     const RotaryTensor t = c.t[which];
     const Place p = places.p[which];
     const int part = block % p.parts;
@@ -65,50 +71,41 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryCall c, RotaryPl
     const int tokens = min(p.tokens, c.tokens - token0);
     const int units = units_of(p), per_token = t.heads * units;
     // the workgroup's units: `count` from unit `skipped` of head `head0` on
-    const int begin = part * kThreads * kUnits, head0 = begin / units, skipped = begin - head0 * units;
-    const int count = min(tokens * per_token - begin, kThreads * kUnits);
+    const int begin = part * kThreads, head0 = begin / units, skipped = begin - head0 * units;
+    const int count = min(tokens * per_token - begin, kThreads);
 
-    // this thread's units: read before the sines are formed
-    Raw<BF, V> a[kUnits], b[kUnits];
-    int table_at[kUnits];  // -1: copied
-    int64_t to[kUnits];
-    int na[kUnits], nb[kUnits], apart[kUnits];
-#pragma unroll
-    for (int q = 0; q < kUnits; ++q) {
-        const int local = q * kThreads + (int)threadIdx.x;
-        const bool has = local < count;
-        const int v = skipped + (has ? local : 0);
-        const int token = divided(v, p.per_token), r = v - token * per_token;
-        const int h = divided(r, p.per_head), i = r - h * units, head = head0 + h;
-        int first, n;  // the unit's first element, and those that its part has from there on
-        table_at[q] = -1;
-        if (i < p.turning) {
-            table_at[q] = token * (V / 2) * p.turning + i;
-            first = c.first + (INTER && !WHOLE ? 2 * V : V) * i;
-            n = (INTER && !WHOLE ? 2 : 1) * (c.pairs - i * V);
-            apart[q] = INTER && !WHOLE ? V : c.pairs;
-        } else {
-            const bool left = i < p.turning + p.before;
-            const int k = (WHOLE ? V : 2 * V) * (i - p.turning - (left ? 0 : p.before));
-            first = left ? k : c.first + 2 * c.pairs + k;
-            n = (left ? c.first : c.head_dim) - first;
-            apart[q] = !WHOLE ? V : V * (left ? p.before : p.after);
-        }
-        na[q] = has ? n : 0;
-        nb[q] = has ? n - (INTER || table_at[q] < 0 ? V : 0) : 0;  // (!WHOLE)
-        const int64_t at = (token0 + token) * t.x_token + head * t.x_head + first;
-        to[q] = (token0 + token) * t.y_token + head * t.y_head + first;
-        // (WHOLE: a thread without a unit reads the workgroup's first)
-        a[q] = load_raw<BF, V, WHOLE, NT>(t.x, at, na[q]);
-        b[q] = load_raw<BF, V, WHOLE, NT>(t.x, at + apart[q], nb[q]);
+    // this thread's unit, read before the sines are formed; one without any reads
+    // the workgroup's first
+    const bool has = (int)threadIdx.x < count;
+    const int v = skipped + (has ? (int)threadIdx.x : 0);
+    const int token = divided(v, p.per_token), r = v - token * per_token;
+    const int h = divided(r, p.per_head), i = r - h * units, head = head0 + h;
+    const bool turns = i < p.turning;
+    int first, n, apart;  // the unit's first element, those that its part has from there on, its other run
+    if (turns) {
+        first = c.first + (INTER && !WHOLE ? 2 * V : V) * i;
+        n = (INTER && !WHOLE ? 2 : 1) * (c.pairs - i * V);
+        apart = INTER && !WHOLE ? V : c.pairs;
+    } else {
+        const bool left = i < p.turning + p.before;
+        const int k = (WHOLE ? V : 2 * V) * (i - p.turning - (left ? 0 : p.before));
+        first = left ? k : c.first + 2 * c.pairs + k;
+        n = (left ? c.first : c.head_dim) - first;
+        apart = !WHOLE ? V : V * (left ? p.before : p.after);
     }
+    // (what the two runs have, where units may be cut short)
+    const int na = has ? n : 0, nb = has ? n - (INTER || !turns ? V : 0) : 0;
+    const int64_t from = (token0 + token) * t.x_token + head * t.x_head + first;
+    const int64_t to = (token0 + token) * t.y_token + head * t.y_head + first;
+    const Raw<BF, V> a = load_raw<BF, V, WHOLE, NT>(t.x, from, na);
+    const Raw<BF, V> b = load_raw<BF, V, WHOLE, NT>(t.x, from + apart, nb);
 
-    for (int i = threadIdx.x; i < tokens * c.pairs; i += kThreads) {
-        const int k = (uint32_t)i / (uint32_t)c.pairs, pair = i - k * c.pairs;
+    for (int j = threadIdx.x; j < tokens * c.pairs; j += kThreads) {
+        const int k = (uint32_t)j / (uint32_t)c.pairs, pair = j - k * c.pairs;
         constexpr double kPerTurn = 0.15915494309189533577;  // 1 / (2 pi)
-        const double turns = gld(c.positions + token0 + k) * (gld(c.frequencies + pair) * kPerTurn);
+        const double angle = gld(c.positions + token0 + k) * (gld(c.frequencies + pair) * kPerTurn);
         float s, co;
-        sincospif(2.f * (float)(turns - rint(turns)), &s, &co);
+        sincospif(2.f * (float)(angle - rint(angle)), &s, &co);
         int unit = pair / V, e = pair % V;
         if (INTER && WHOLE) {
             const int half = pair >= c.pairs / 2, of = pair - half * (c.pairs / 2);
@@ -119,46 +116,43 @@ __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryCall c, RotaryPl
             make_float2(co * c.scale, (c.transpose ? -s : s) * c.scale);
     }
     __syncthreads();
+    if (!has) return;
 
+    float x[V], y[V];
 #pragma unroll
-    for (int q = 0; q < kUnits; ++q) {
-        float x[V], y[V];
+    for (int e = 0; e < V; ++e) {
+        x[e] = a.at(e);
+        y[e] = b.at(e);
+    }
+    if (turns) {
+        // (pairs behind the last, in a unit that is cut short, turn by anything)
+        const float4* cs = reinterpret_cast<const float4*>(table) + token * (V / 2) * p.turning + i;
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            x[e] = a[q].at(e);
-            y[e] = b[q].at(e);
-        }
-        if (table_at[q] >= 0) {
-            // (pairs behind the last, in a unit that is cut short, turn by anything)
-            const float4* cs = reinterpret_cast<const float4*>(table) + table_at[q];
-#pragma unroll
-            for (int k = 0; k < V / 2; ++k) {
-                const float4 f = cs[k * p.turning];  // cosine, sine of pairs 2 k and 2 k + 1
-                auto turn = [](float& u, float& v, float co, float s) {
-                    const float w = u;
-                    u = w * co - v * s;
-                    v = v * co + w * s;
-                };
-                if (INTER) {
-                    float* z = k < V / 4 ? x + 4 * k : y + 4 * k - V;
-                    turn(z[0], z[1], f.x, f.y);
-                    turn(z[2], z[3], f.z, f.w);
-                } else {
-                    turn(x[2 * k], y[2 * k], f.x, f.y);
-                    turn(x[2 * k + 1], y[2 * k + 1], f.z, f.w);
-                }
+        for (int k = 0; k < V / 2; ++k) {
+            const float4 f = cs[k * p.turning];  // cosine, sine of pairs 2 k and 2 k + 1
+            auto turn = [](float& u, float& w, float co, float s) {
+                const float old = u;
+                u = old * co - w * s;
+                w = w * co + old * s;
+            };
+            if (INTER) {
+                float* z = k < V / 4 ? x + 4 * k : y + 4 * k - V;
+                turn(z[0], z[1], f.x, f.y);
+                turn(z[2], z[3], f.z, f.w);
+            } else {
+                turn(x[2 * k], y[2 * k], f.x, f.y);
+                turn(x[2 * k + 1], y[2 * k + 1], f.z, f.w);
             }
         }
-        if (WHOLE && na[q] <= 0) continue;
-        store_unit<V, BF, WHOLE>(t.y, to[q], na[q], x);
-        store_unit<V, BF, WHOLE>(t.y, to[q] + apart[q], nb[q], y);
     }
+    store_unit<V, BF, WHOLE>(t.y, to, na, x);
+    store_unit<V, BF, WHOLE>(t.y, to + apart, nb, y);
 }
 
 // The plan of a call: false where its workgroups cannot be numbered.
 template <bool BF>
 bool plan(const RotaryCall& c, RotaryPlaces* places, int64_t* blocks, bool* whole, bool* nontemporal) {
-    constexpr int V = BF ? 8 : 4, most = kThreads * kUnits;
+    constexpr int V = BF ? 8 : 4, most = kThreads;
     int64_t bytes = 0;
     *blocks = 0;
     *whole = c.pairs % V == 0;

@@ -49,13 +49,21 @@ __device__ __forceinline__ Raw<BF, V> load_raw(const void* base, int64_t off, in
     } else {
 #pragma unroll
         for (int i = 0; i < Raw<BF, V>::W; ++i) r.w[i] = 0;
+        if (left > 0) {
+            // the last element in place of those behind it: all loads in flight at once
+            uint32_t v[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-            if (e < left) {
+            for (int e = 0; e < V; ++e) {
+                const int64_t at = off + (e < left ? e : left - 1);
+                v[e] = BF ? gld(reinterpret_cast<const uint16_t*>(base) + at) : gld(reinterpret_cast<const uint32_t*>(base) + at);
+            }
+#pragma unroll
+            for (int e = 0; e < V; ++e) {
+                const uint32_t w = e < left ? v[e] : 0;
                 if (BF)
-                    r.w[e / 2] |= (uint32_t)gld(reinterpret_cast<const uint16_t*>(base) + off + e) << 16 * (e & 1);
+                    r.w[e / 2] |= w << 16 * (e & 1);
                 else
-                    r.w[e] = gld(reinterpret_cast<const uint32_t*>(base) + off + e);
+                    r.w[e] = w;
             }
         }
     }
