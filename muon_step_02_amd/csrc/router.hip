@@ -487,6 +487,7 @@ template <bool BF, int L, int C>
 __global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradCall c) {
     __shared__ double red[kWaves];
     constexpr int TEAMS = 64 / L, V = BF ? 8 : 4;
+    constexpr int K = C * L < kRouterMaxChoices ? C * L : kRouterMaxChoices, Q = (K + L - 1) / L;  // choices; of a lane
     const int lane = threadIdx.x & 63, l = lane % L, team = lane / L, wave = threadIdx.x >> 6;
     const float n = (float)max(gld(c.live), 1);
     // every token's gradient of the balance loss by its probabilities
@@ -505,60 +506,75 @@ __global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradCall c)
          first += (int64_t)gridDim.x * kWaves * TEAMS) {
         const int64_t t = first + team;
         const bool has = t < c.tokens;
-        const void* row = c.logits;
         const int64_t at = (has ? t : 0) * c.ld;
-        float z[C], p[C], g[C], add[C];
-        load_logits<BF, C>(row, at + l * C, has ? c.experts - l * C : 0, z);
+        float z[C], p[C], own[C];  // own: the gates' part of what the expert gets
+        load_logits<BF, C>(c.logits, at + l * C, has ? c.experts - l * C : 0, z);
         const Softmax x = softmax<L, C>(z, p);
         const float inv = x.live ? 1.f / x.total : 0.f;
         const float lse = x.live ? x.top + logf(x.total) : 0.f;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
             p[i] *= inv;
-            g[i] = share[i];
-            add[i] = 0.f;
+            own[i] = 0.f;
         }
-        if (c.dgates && has) {
-            const int32_t* chosen = c.chosen + t * c.top_k;
-            const float* d = c.dgates + t * c.top_k;
-            // renormalised gates are a softmax over the chosen logits
-            float top = -INFINITY, sum = 0.f, dot = 0.f;
-            auto logit = [&](int e) {
-                return BF ? bf16_bits_to_f32(gld(reinterpret_cast<const uint16_t*>(row) + at + e))
-                          : gld(reinterpret_cast<const float*>(row) + at + e);
-            };
-            auto is = [&](int e) { return e >= 0 && e < c.experts; };
-            if (c.renormalize) {
-                for (int j = 0; j < c.top_k; ++j) {
-                    const int e = gld(chosen + j);
-                    if (is(e)) top = fmaxf(top, logit(e));
-                }
-                for (int j = 0; j < c.top_k; ++j) {
-                    const int e = gld(chosen + j);
-                    if (!is(e)) continue;
-                    const float w = exp_of(logit(e) - top);
-                    sum += w;
-                    dot = fmaf(w, gld(d + j), dot);
-                }
-                dot /= sum;
-            }
-            for (int j = 0; j < c.top_k; ++j) {
-                const int e = gld(chosen + j);
-                if (!is(e)) continue;
-                const float v = gld(d + j);
-                const float w = c.renormalize ? exp_of(logit(e) - top) / sum * (v - dot) : v;
+        if (c.dgates) {
+            // a lane has every L-th choice: its expert and its gate's gradient
+            int e[Q];
+            float d[Q];
 #pragma unroll
-                for (int i = 0; i < C; ++i)
-                    if (l * C + i == e) (c.renormalize ? add[i] : g[i]) += w;
+            for (int q = 0; q < Q; ++q) {
+                const int j = q * L + l;
+                const bool there = has && j < c.top_k;
+                e[q] = there ? gld(c.chosen + t * c.top_k + j) : -1;
+                d[q] = there ? gld(c.dgates + t * c.top_k + j) : 0.f;
+                if (e[q] >= c.experts) e[q] = -1;
+            }
+            if (c.renormalize) {
+                // the gates are a softmax over the chosen logits
+                float w[Q], most = -INFINITY, sum = 0.f, along = 0.f;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    w[q] = -INFINITY;
+                    if (e[q] >= 0)
+                        w[q] = BF ? bf16_bits_to_f32(gld(reinterpret_cast<const uint16_t*>(c.logits) + at + e[q]))
+                                  : gld(reinterpret_cast<const float*>(c.logits) + at + e[q]);
+                    most = fmaxf(most, w[q]);
+                }
+                most = team_reduce<L>(most, [](float a, float b) { return fmaxf(a, b); });
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    w[q] = e[q] >= 0 ? exp_of(w[q] - most) : 0.f;
+                    sum += w[q];
+                    along = fmaf(w[q], d[q], along);
+                }
+                sum = team_sum<L>(sum);
+                along = team_sum<L>(along);
+#pragma unroll
+                for (int q = 0; q < Q; ++q) d[q] = e[q] >= 0 ? w[q] / sum * (d[q] - along / sum) : 0.f;
+            }
+            // to the lanes that have the experts, one choice after the other
+#pragma unroll
+            for (int q = 0; q < Q; ++q) {
+                const int n_of = min(L, c.top_k - q * L);
+                for (int k = 0; k < n_of; ++k) {
+                    const int from = (lane - l + k) << 2;
+                    const int to = L > 1 ? __builtin_amdgcn_ds_bpermute(from, e[q]) : e[q];
+                    const float v = L > 1 ? __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, d[q])))
+                                          : d[q];
+#pragma unroll
+                    for (int i = 0; i < C; ++i) own[i] += l * C + i == to ? v : 0.f;
+                }
             }
         }
+        // by the probabilities; renormalised gates have none of it
         float dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < C; ++i) dot = fmaf(p[i], g[i], dot);
-        dot = team_sum<L>(dot);
+        for (int i = 0; i < C; ++i) dot = fmaf(p[i], share[i] + (c.renormalize ? 0.f : own[i]), dot);
+        dot = team_sum<L>(dot) - zn * lse;
         float o[C];
 #pragma unroll
-        for (int i = 0; i < C; ++i) o[i] = fmaf(p[i], g[i] - dot + zn * lse, add[i]);
+        for (int i = 0; i < C; ++i)
+            o[i] = c.renormalize ? fmaf(p[i], share[i] - dot, own[i]) : p[i] * (share[i] + own[i] - dot);
         if (has)
 #pragma unroll
             for (int q = 0; q < C; q += V)
