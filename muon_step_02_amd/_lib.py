@@ -186,6 +186,9 @@ class MuonHeads(ctypes.Structure):
     ]
 
 
+_HEADS_OF = [MuonHeads * n for n in range(5)]
+
+
 class MuonLayernorm(ctypes.Structure):
     _fields_ = [
         ("weight", ctypes.c_void_p),
@@ -779,15 +782,14 @@ def _queue(h, stream, *tensors):
     return _stream_on(stream, tensors[0].device, h)
 
 
-def _heads(t, what):
-    """Descriptor of a (tokens, heads, width) tensor, or of a (tokens, width)
-    one as one head a token."""
-    n = t.dim()
-    if n == 3:
-        tokens, heads, width = t.shape
+def _heads(t, shape, what):
+    """Descriptor of a (tokens, heads, width) tensor of that shape, or of a
+    (tokens, width) one as one head a token."""
+    if len(shape) == 3:
+        tokens, heads, width = shape
         s, sh, sw = t.stride()
-    elif n == 2:
-        (tokens, width), heads = t.shape, 1
+    elif len(shape) == 2:
+        (tokens, width), heads = shape, 1
         s, sw = t.stride()
     else:
         raise ValueError("%s must be (tokens, heads, width) or (tokens, width)" % what)
@@ -805,7 +807,7 @@ def _vector(t, numel, dtype, what):
     """Pointer of a contiguous tensor of `numel` values (None: not given)."""
     if t is None:
         return None
-    if t.numel() != numel or t.dtype != dtype or not t.is_contiguous():
+    if t.numel() != numel or t.dtype is not dtype or not t.is_contiguous():
         raise ValueError("%s must be contiguous, %d values of %s" % (what, numel, dtype))
     return t.data_ptr()
 
@@ -829,9 +831,9 @@ def muon_layernorm_forward(h, x, y, weight=None, bias=None, mean=None, rstd=None
     import torch
     queue = _queue(h, stream, x, y, weight, bias, mean, rstd)
     shape = x.shape
-    if y.shape != shape or y.dtype != x.dtype:
+    if y.shape != shape or y.dtype is not x.dtype:
         raise ValueError("x and y differ in shape or type")
-    hx, hy, cols = _heads(x, "x"), _heads(y, "y"), shape[-1]
+    hx, hy, cols = _heads(x, shape, "x"), _heads(y, shape, "y"), shape[-1]
     pw, pb, wide = _pair(weight, bias, cols, "weight and bias")
     rows, f32 = shape[0] * hx.heads, torch.float32
     n = MuonLayernorm(pw, pb, shape[0], cols, _dt(x), wide, 1 if center else 0, eps)
@@ -843,7 +845,7 @@ def muon_layernorm_workspace_size(h, x):
     """Workspace bytes of :func:`muon_layernorm_grad` for an ``x`` of this shape and type."""
     sz = ctypes.c_size_t()
     n = MuonLayernorm(None, None, x.shape[0], x.shape[-1], _dt(x), MUON_F32, 1, 0.0)
-    _check(load().muon_layernorm_workspace_size(h, n, _heads(x, "x").heads, sz), "muon_layernorm_workspace_size")
+    _check(load().muon_layernorm_workspace_size(h, n, _heads(x, x.shape, "x").heads, sz), "muon_layernorm_workspace_size")
     return sz.value
 
 
@@ -857,18 +859,18 @@ def muon_layernorm_grad(h, x, dy, rstd, workspace, mean=None, weight=None, dx=No
     queue = _queue(h, stream, x, dy, rstd, workspace, mean, weight, dx, dweight, dbias)
     shape, dtype = x.shape, x.dtype
     for t in (dy, dx):
-        if t is not None and (t.shape != shape or t.dtype != dtype):
+        if t is not None and (t.shape != shape or t.dtype is not dtype):
             raise ValueError("x, dy and dx differ in shape or type")
     if center and mean is None:
         raise ValueError("a centered norm needs its mean")
-    hx, cols, f32 = _heads(x, "x"), shape[-1], torch.float32
+    hx, cols, f32 = _heads(x, shape, "x"), shape[-1], torch.float32
     rows = shape[0] * hx.heads
     pw, _, wide = _pair(weight, None, cols, "weight")
     pdw, pdb, grad = _pair(dweight, dbias, cols, "dweight and dbias")
     n = MuonLayernorm(pw, None, shape[0], cols, _dt(x), wide, 1 if center else 0, 0.0)
     _check(load().muon_layernorm_grad(
-        h, n, hx, _heads(dy, "dy"), _vector(mean, rows, f32, "mean"), _vector(rstd, rows, f32, "rstd"),
-        _heads(dx, "dx") if dx is not None else None, pdw, pdb, grad, 1 if accumulate else 0, workspace.data_ptr(),
+        h, n, hx, _heads(dy, shape, "dy"), _vector(mean, rows, f32, "mean"), _vector(rstd, rows, f32, "rstd"),
+        _heads(dx, shape, "dx") if dx is not None else None, pdw, pdb, grad, 1 if accumulate else 0, workspace.data_ptr(),
         _nbytes(workspace), queue), "muon_layernorm_grad")
 
 
@@ -900,27 +902,30 @@ def muon_rotary(h, x, y, positions, frequencies, first=0, interleaved=False, sca
         raise ValueError("expected one to four tensors and as many outputs")
     queue = _queue(h, stream, positions, frequencies, *xs, *ys)
     x0, pairs = xs[0], frequencies.numel()
-    tokens, dim, dtype = x0.shape[0], x0.shape[-1], x0.dtype
-    hs = MuonHeads * n
-    hx, hy = hs(), hs()
-    for i in range(n):
-        a, b = xs[i], ys[i]
+    shape, dtype = x0.shape, x0.dtype
+    tokens, dim = shape[0], shape[-1]
+    hx, hy = [], []
+    for a, b in zip(xs, ys):
         shape = a.shape
-        if b.shape != shape or shape[0] != tokens or shape[-1] != dim or a.dtype != dtype or b.dtype != dtype:
+        if b.shape != shape or shape[0] != tokens or shape[-1] != dim or a.dtype is not dtype or b.dtype is not dtype:
             raise ValueError("the tensors differ in tokens, head size or type, or from their outputs in shape")
-        hx[i], hy[i] = _heads(a, "x"), _heads(b, "y")
+        hx.append(_heads(a, shape, "x"))
+        hy.append(_heads(b, shape, "y"))
+    hs = _HEADS_OF[n]
     p = MuonPositions(_vector(positions, tokens, torch.int32, "positions"),
                       _vector(frequencies, pairs, torch.float64, "frequencies"), tokens, dim, first, pairs,
                       1 if interleaved else 0, _dt(x0), scale)
-    _check(load().muon_rotary(h, p, hx, hy, n, 1 if transpose else 0, queue), "muon_rotary")
+    _check(load().muon_rotary(h, p, hs(*hx), hs(*hy), n, 1 if transpose else 0, queue), "muon_rotary")
 
 
 def _router(logits, top_k, renormalize):
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be 2D with unit column stride")
-    tokens, experts = logits.shape
-    return MuonRouter(logits.data_ptr(), tokens, logits.stride(0) if tokens > 1 else experts, experts, top_k,
-                      _dt(logits), 1 if renormalize else 0), tokens, experts
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2D")
+    (tokens, experts), (ld, step) = logits.shape, logits.stride()
+    if step != 1 and experts > 1:
+        raise ValueError("logits need unit column stride")
+    return MuonRouter(logits.data_ptr(), tokens, ld if tokens > 1 else experts, experts, top_k, _dt(logits),
+                      1 if renormalize else 0), tokens, experts
 
 
 def _top_k(chosen):
@@ -971,7 +976,7 @@ def muon_router_grad(h, logits, chosen, counts, live, dlogits, dgates=None, bala
     queue = _queue(h, stream, logits, chosen, counts, live, dlogits, dgates)
     top_k = _top_k(chosen)
     r, tokens, experts = _router(logits, top_k, renormalize)
-    if dlogits.shape != logits.shape or dlogits.dtype != logits.dtype or (experts > 1 and dlogits.stride(1) != 1):
+    if dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or (experts > 1 and dlogits.stride(1) != 1):
         raise ValueError("dlogits must have the logits' shape and type, and unit column stride")
     n = tokens * top_k
     _check(load().muon_router_grad(h, r, _vector(chosen, n, i32, "chosen"), _vector(counts, experts, i32, "counts"),

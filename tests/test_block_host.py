@@ -338,19 +338,23 @@ def test_binding_refuses_tensors_on_the_host():
 
 def test_binding_describes_tensors():
     from muon_step_02_amd import _lib
+
+    def heads(t):
+        return _lib._heads(t, t.shape, "x")
+
     t = torch.zeros(6, 4, 10)
-    d = _lib._heads(t[:, 1:3, 2:8], "x")
+    d = heads(t[:, 1:3, 2:8])
     assert (d.token, d.head, d.heads, d.data) == (40, 10, 2, t.data_ptr() + 4 * 12)
-    d = _lib._heads(t[:, 0], "x")
+    d = heads(t[:, 0])
     assert (d.token, d.head, d.heads) == (40, 10, 1)
-    d = _lib._heads(t[:1], "x")
+    d = heads(t[:1])
     assert (d.token, d.head, d.heads) == (40, 10, 4)
-    d = _lib._heads(t.transpose(0, 1), "x")
+    d = heads(t.transpose(0, 1))
     assert (d.token, d.head, d.heads) == (10, 40, 6)
     with pytest.raises(ValueError):
-        _lib._heads(t.transpose(1, 2), "x")
+        heads(t.transpose(1, 2))
     with pytest.raises(ValueError):
-        _lib._heads(t[0, 0], "x")
+        heads(t[0, 0])
     for bad in (t[:, 0, 0], torch.zeros(5), torch.zeros(6, dtype=torch.float64)):
         with pytest.raises(ValueError):
             _lib._vector(bad, 6, torch.float32, "w")
