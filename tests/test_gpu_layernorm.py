@@ -357,3 +357,50 @@ def test_streams_and_a_captured_graph():
         torch.cuda.synchronize()
         for a, b in zip(outs, _forward(x, w) + _grad(*args, True)):
             assert torch.equal(a, b)
+
+
+# ---- large tensors --------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,rows,cols", [(BF16, 500003, 128), (F32, 200001, 130), (BF16, 70001, 1000),
+                                             (F32, 26001, 1001), (BF16, 9001, 7168)])
+def test_large_tensors_are_their_parts(dtype, rows, cols):
+    # beyond 96 MiB rows are read around the caches, and workgroups take many of them
+    gen = _gen(rows)
+    x, dy = (torch.randint(-4, 5, (rows, cols), generator=gen, device=DEV, dtype=torch.int8).to(dtype) for _ in range(2))
+    assert x.nbytes >= 96 << 20
+    w, b = _weights(gen, cols, F32)
+    y, mean, rstd = _forward(x, w, b)
+    one = torch.ones(rows, device=DEV)
+    dx, dw, db = _grad(x, dy, mean, one, w, True)
+    step = 7001
+    for a in range(0, rows, rows // 3):
+        cut = slice(a, min(a + step, rows))
+        for got, want in zip((y, mean, rstd), _forward(x[cut], w, b)):
+            assert torch.equal(got[cut], want)
+        assert torch.equal(dx[cut], _grad(x[cut], dy[cut], mean[cut], one[cut], w, True)[0])
+    # whole numbers below 2^24: exact in any order
+    zero = torch.zeros(rows, device=DEV)
+    _, dw, db = _grad(x, dy, zero, one, None, True)
+    assert torch.equal(db, dy.sum(0, dtype=torch.float64).float())
+    want = torch.zeros(cols, device=DEV, dtype=torch.float64)
+    for a in range(0, rows, 100000):
+        want += (x[a:a + 100000].float() * dy[a:a + 100000].float()).sum(0, dtype=torch.float64)
+    assert torch.equal(dw, want.float())
+
+
+def test_rows_far_apart():
+    # 2^31 elements and more between a tensor's first and last row
+    cols, far = 200, (1 << 30) + 8
+    buf = torch.zeros(2 * far + cols, device=DEV, dtype=BF16)
+    x = torch.as_strided(buf, (3, cols), (far, 1))
+    small = _values(_gen(1), 3, cols, dtype=BF16)
+    w, b = _weights(_gen(2), cols, BF16)
+    x.copy_(small)
+    want = _forward(small, w, b)
+    for got, ref in zip(_forward(x, w, b), want):
+        assert torch.equal(got, ref)
+    args = small, _values(_gen(3), 3, cols, dtype=BF16), want[1], want[2], w
+    ref = _grad(*args, True)
+    into = torch.as_strided(buf, (3, cols), (far, 1))
+    got = _grad(x, *args[1:], True, dx=into)
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))

@@ -206,3 +206,35 @@ def test_streams_and_a_captured_graph():
         for x, y in zip((q, k), outs):
             assert torch.equal(y, _turn(x, pos, freq))
     mu.muon_rotary(h, q[:0], outs[0][:0], pos[:0], freq)
+
+
+@pytest.mark.parametrize("dtype,tokens,interleaved,first", [(BF16, 20011, False, 0), (F32, 9001, True, 0),
+                                                            (BF16, 20011, True, 32), (F32, 9001, False, 3)])
+def test_large_tensors_are_their_parts(dtype, tokens, interleaved, first):
+    # beyond 96 MiB the tensors are read around the caches
+    gen, freq = _gen(tokens), mu.muon_rotary_frequencies(32).to(DEV)
+    q, k = _values(gen, tokens, 24, 128, dtype), _values(gen, tokens, 3, 128, dtype)
+    assert q.nbytes + k.nbytes >= 96 << 20
+    pos = _positions(gen, tokens)
+    kw = dict(first=first, interleaved=interleaved)
+    y = [torch.zeros_like(q), torch.zeros_like(k)]
+    mu.muon_rotary(Handle.get(), [q, k], y, pos, freq, **kw)
+    for a in range(0, tokens, tokens // 3):
+        cut = slice(a, a + 1001)
+        for x, got in zip((q, k), y):
+            assert torch.equal(got[cut], _turn(x[cut], pos[cut].contiguous(), freq, **kw))
+    mu.muon_rotary(Handle.get(), [q, k], [q, k], pos, freq, **kw)
+    assert torch.equal(q, y[0]) and torch.equal(k, y[1])
+
+
+def test_tokens_far_apart():
+    # 2^31 elements and more between a tensor's first and last token
+    far, freq = (1 << 30) + 8, mu.muon_rotary_frequencies(32).to(DEV)
+    buf = torch.zeros(2 * far + 4 * 64, device=DEV, dtype=BF16)
+    x = torch.as_strided(buf, (3, 4, 64), (far, 64, 1))
+    small = _values(_gen(1), 3, 4, 64, BF16)
+    x.copy_(small)
+    pos = _positions(_gen(2), 3)
+    want = _turn(small, pos, freq)
+    assert torch.equal(_turn(x, pos, freq, out=torch.zeros_like(small)), want)
+    assert torch.equal(_turn(x, pos, freq, out=x), want)

@@ -117,6 +117,39 @@ def test_tokens(tokens, dtype):
     _check(_logits(tokens, tokens, 10, dtype), 3, True)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_tokens(dtype):
+    # more workgroups than the sums between them take at once
+    _check(_logits(3, 300001, 5, dtype), 2, True)
+    _check(_logits(4, 70001, 200, dtype), 8)
+
+
+def test_tokens_far_apart():
+    # 2^31 logits and more between the first token's and the last one's
+    far = (1 << 30) + 8
+    buf = torch.zeros(2 * far + 80, device=DEV, dtype=BF16)
+    z = torch.as_strided(buf, (3, 80), (far, 1))
+    small = _logits(5, 3, 80, BF16)
+    z.copy_(small)
+    want, got = _route(small, 8), _route(z, 8)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    d = torch.randn(3, 8, generator=_gen(1), device=DEV)
+    ref = _grad(small, want, d, 0.1, 0.1, True)
+    assert torch.equal(_grad(z, want, d, 0.1, 0.1, True), ref)
+    wide = torch.as_strided(torch.zeros(2 * far + 80, device=DEV, dtype=BF16), (3, 80), (far, 1))
+    assert torch.equal(_grad(small, want, d, 0.1, 0.1, True, out=wide), ref)
+
+
+def test_logits_next_to_zero_keep_their_order():
+    # values that have no normal fp32 form, of both signs, with ties
+    z = torch.randint(-3, 4, (130, 30), generator=_gen(6), device=DEV).float() * 1e-42
+    assert int((z != 0).sum()) > 0
+    got = _route(z, 6)
+    by = np.argsort(-z.double().cpu().numpy(), axis=1, kind="stable")[:, :6]
+    assert np.array_equal(got["chosen"].cpu().numpy(), by)
+
+
 def test_no_tokens():
     got = _route(_logits(1, 0, 64, F32), 8)
     for name in ("counts", "offsets", "live", "losses"):
@@ -158,6 +191,30 @@ def test_experts_out_of_reach_and_tokens_without_any(dtype):
             assert got["chosen"][5].tolist() == [0, -1, -1, -1, -1, -1] and float(got["gates"][5, 0]) == 1.0
         got = _check(torch.full_like(z, NEG), 6)
         assert float(got["losses"].abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("experts", [129, 256, 300, 512, 700, 1024])
+def test_few_choices_of_many_experts(experts, dtype):
+    # up to 8 choices are found at once, from up to 16 logits that reach a bound
+    gen = _gen(experts)
+    for k in (1, 3, 7, 8):
+        for values in (30, 100, 250):       # some of the largest are equal
+            _check(torch.randint(0, values, (90, experts), generator=gen, device=DEV).to(dtype), k)
+        z = _logits(k, 90, experts, dtype)
+        z[::3] = NEG                        # tokens without any, beside others
+        z[1::6, 5:] = NEG                   # with fewer than the choices
+        z[2::6, :experts - 17] = NEG        # with all of them close together
+        z[4::6] = torch.where(torch.arange(experts, device=DEV) % 16 == 3, z[4::6], NEG)
+        for renormalize in (False, True):
+            _check(z, k, renormalize)
+        want = _route(z, k)
+        z[7, 100] = float("nan")
+        got = _route(z, k)
+        assert bool(torch.isnan(got["gates"][7]).all()) and not bool((got["chosen"][7] == 100).any())
+        keep = torch.arange(90, device=DEV) != 7
+        for n in ("chosen", "gates"):
+            assert torch.equal(got[n][keep], want[n][keep])
 
 
 def test_values_far_apart_and_infinite():
