@@ -20,6 +20,7 @@
 // lies behind a row reads as zero and is not written, a row that is not there
 // has no length, and the last unit of a row whose length is no multiple of a
 // unit starts earlier (its first elements are its neighbour's, computed twice).
+#include <algorithm>
 #include <type_traits>
 
 #include "block.h"
@@ -85,11 +86,14 @@ __device__ __forceinline__ void load_weight(const void* w, bool bf, int at, int 
     }
 }
 
+// How rows end: with a whole unit; with one that starts earlier, so that it ends
+// with the row; or within their only one.
+enum RowEnd { kWhole, kShifted, kShort };
+
 // Which elements of a row a lane of a team of L has: R units of V.  Unit i starts
-// at column at[i]; its first skip[i] elements are another unit's too (V: all are,
-// or there is no such unit).  EVEN: rows are whole units, nothing is skipped, and
-// at[i] >= cols where there is none.
-template <bool BF, bool EVEN, int L, int R>
+// at column at[i]; kShifted: its first skip[i] elements are another unit's too (V:
+// there is no such unit).
+template <bool BF, RowEnd END, int L, int R>
 struct Share {
     static constexpr int V = BF ? 8 : 4;
     static constexpr int kNowhere = 1 << 24;  // behind every row
@@ -100,29 +104,28 @@ struct Share {
             const int c = (i * L + l) * V;
             at[i] = c;
             skip[i] = 0;
-            if (!EVEN && L >= 64 && c + V > cols) {
-                at[i] = c < cols ? cols - V : kNowhere;
+            if (END == kShifted && c + V > cols) {
+                at[i] = c < cols ? cols - V : L >= 64 ? kNowhere : 0;
                 skip[i] = c < cols ? c - (cols - V) : V;
             }
         }
     }
     // whether element e of unit i is in the row, and this lane's to count
     __device__ __forceinline__ bool mine(int i, int e, int cols) const {
-        if (EVEN) return at[i] < cols;
-        return L >= 64 ? e >= skip[i] : at[i] + e < cols;
+        return END == kShifted ? e >= skip[i] : END == kWhole ? at[i] < cols : at[i] + e < cols;
     }
-    // a unit that a row of a team of this size may not have (those of the second
-    // half of L * R: smaller teams take rows without them)
-    static constexpr bool maybe(int i) { return R == 1 || 2 * i >= R; }
+    // a unit that a row of a team of this size may not have: smaller teams take the
+    // rows that end before these
+    static constexpr bool maybe(int i) { return R == 1 || 2 * i + 1 >= R; }
 };
 
 // A row, as it is in memory.
-template <bool BF, bool EVEN, int L, int R>
+template <bool BF, RowEnd END, int L, int R>
 struct Row {
     static constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4;
     Raw<BF, V> u[R];
     template <bool NT>
-    __device__ __forceinline__ void read(const void* base, int64_t off, int cols, const Share<BF, EVEN, L, R>& s, bool has) {
+    __device__ __forceinline__ void read(const void* base, int64_t off, int cols, const Share<BF, END, L, R>& s, bool has) {
         if constexpr (L >= 64) {
             const auto r = row_resource(reinterpret_cast<const char*>(base) + off * ES, has ? cols * ES : 0);
 #pragma unroll
@@ -135,13 +138,14 @@ struct Row {
 #pragma unroll
             for (int i = 0; i < R; ++i) {
                 const int left = has ? cols - s.at[i] : 0;
-                if (!EVEN) {
+                if (END == kShort) {
                     u[i] = load_raw<BF, V, false, NT>(base, off + s.at[i], left);
                 } else {
                     // from the row's start where there is no such unit
-                    u[i] = load_raw<BF, V, true, NT>(base, off + (left > 0 ? s.at[i] : 0), V);
+                    const bool there = END == kShifted ? has && s.skip[i] < V : left > 0;
+                    u[i] = load_raw<BF, V, true, NT>(base, off + (there ? s.at[i] : 0), V);
 #pragma unroll
-                    for (int k = 0; k < Raw<BF, V>::W; ++k) u[i].w[k] = left > 0 ? u[i].w[k] : 0;
+                    for (int k = 0; k < Raw<BF, V>::W; ++k) u[i].w[k] = there ? u[i].w[k] : 0;
                 }
             }
         }
@@ -150,7 +154,7 @@ struct Row {
     // branch there, not a kernel: the aux bits of the two loads keep the compiler
     // from making one of them).
     template <bool NT>
-    __device__ __forceinline__ void load(const void* base, int64_t off, int cols, const Share<BF, EVEN, L, R>& s, bool has,
+    __device__ __forceinline__ void load(const void* base, int64_t off, int cols, const Share<BF, END, L, R>& s, bool has,
                                          bool nontemporal) {
         if (NT || (L >= 64 && nontemporal))
             read<true>(base, off, cols, s, has);
@@ -160,7 +164,7 @@ struct Row {
 };
 
 // Writes v, unit i of a row at a time.
-template <bool BF, bool EVEN, int L, int R>
+template <bool BF, RowEnd END, int L, int R>
 struct Out {
     static constexpr int V = BF ? 8 : 4, ES = BF ? 2 : 4;
     char* p;
@@ -168,7 +172,7 @@ struct Out {
     bool has;
     __device__ __forceinline__ Out(void* base, int64_t off, int cols_, bool has_)
         : p(reinterpret_cast<char*>(base) + off * ES), cols(cols_), has(has_) {}
-    __device__ __forceinline__ void put(int i, const Share<BF, EVEN, L, R>& s, const float* v) const {
+    __device__ __forceinline__ void put(int i, const Share<BF, END, L, R>& s, const float* v) const {
         if constexpr (L >= 64) {
             u32x4 w;
 #pragma unroll
@@ -178,9 +182,9 @@ struct Out {
             __builtin_amdgcn_raw_buffer_store_b128(w, row_resource(p, has ? cols * ES : 0), s.at[i] * ES, 0, 0);
         } else if (has) {
             const int left = cols - s.at[i];
-            if (!EVEN)
+            if (END == kShort)
                 store_unit<V, BF, false>(p, s.at[i], left, v);
-            else if (left > 0)
+            else if (END == kShifted ? s.skip[i] < V : left > 0)
                 store_unit<V, BF, true>(p, s.at[i], V, v);
         }
     }
@@ -259,23 +263,23 @@ __device__ __forceinline__ void walk_rows(int64_t first, int64_t stride, int row
 }
 
 template <int L>
-constexpr int threads_of() { return L > 256 ? L : 256; }
+constexpr int threads_of() { return L > 128 ? L : 256; }
 
-template <bool BF, bool EVEN, int L, int R, bool NT>
+template <bool BF, RowEnd END, int L, int R, bool NT>
 __global__ __launch_bounds__(threads_of<L>()) void norm_forward_kernel(NormCall c) {
     constexpr int V = BF ? 8 : 4, THREADS = threads_of<L>(), TEAMS = THREADS / L;
     __shared__ float red[L > 64 ? 4 * (THREADS / 64) : 1];
     const int l = threadIdx.x % L, team = team_of<L>();
-    const Share<BF, EVEN, L, R> s(l, c.cols);
+    const Share<BF, END, L, R> s(l, c.cols);
     float w[R][V], b[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-        load_weight<V, EVEN || L >= 64>(c.weight, c.weight_bf16, s.at[i], c.cols, 1.f, w[i]);
-        load_weight<V, EVEN || L >= 64>(c.bias, c.weight_bf16, s.at[i], c.cols, 0.f, b[i]);
+        load_weight<V, END != kShort>(c.weight, c.weight_bf16, s.at[i], c.cols, 1.f, w[i]);
+        load_weight<V, END != kShort>(c.bias, c.weight_bf16, s.at[i], c.cols, 0.f, b[i]);
     }
     TeamSum<L, THREADS> sum(red);
     const float n = (float)c.cols;
-    using Buffer = Row<BF, EVEN, L, R>;
+    using Buffer = Row<BF, END, L, R>;
     auto load = [&](Buffer& x, int64_t first) {
         const int64_t row = first + team;
         const bool has = row < c.rows;
@@ -295,7 +299,7 @@ __global__ __launch_bounds__(threads_of<L>()) void norm_forward_kernel(NormCall 
 #pragma unroll
                 for (int e = 0; e < V; ++e)
                     // (what is behind the row reads as zero)
-                    mean += !EVEN && L >= 64 && s.maybe(i) && !s.mine(i, e, c.cols) ? 0.f : v[i][e];
+                    mean += END == kShifted && s.maybe(i) && !s.mine(i, e, c.cols) ? 0.f : v[i][e];
             sum(mean, none, false);
             mean /= n;
         }
@@ -310,7 +314,7 @@ __global__ __launch_bounds__(threads_of<L>()) void norm_forward_kernel(NormCall 
             }
         sum(sq, none, false);
         const float rstd = 1.f / sqrtf(sq / n + c.eps);
-        const Out<BF, EVEN, L, R> out(c.out, has ? row_at(row, c.heads, c.out_token, c.out_head) : 0, c.cols, has);
+        const Out<BF, END, L, R> out(c.out, has ? row_at(row, c.heads, c.out_token, c.out_head) : 0, c.cols, has);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             float o[V];
@@ -339,16 +343,16 @@ __device__ __forceinline__ void put_grad(void* p, bool bf, int accumulate, int c
 }
 
 // Threads of the gradient's workgroups: 256, or two teams that are wider than a
-// wave.  Each team adds its rows to sums of its own, and the workgroup hands on
+// wave, or one.  Each team adds its rows to sums of its own, and the workgroup hands on
 // one sum a column: fewer, wider workgroups leave less to join.
 // (A lane's fp32 rows take twice the registers: 128, which 1024 threads have, are
 // not enough for two teams of 512.)
 template <bool BF, int L>
-constexpr int grad_threads() { return L > 512 || (BF && L > 256) ? 1024 : L > 64 ? 512 : 256; }
+constexpr int grad_threads() { return L <= 64 ? 256 : L <= (BF ? 512 : 256) ? 2 * L : L; }
 
 // dx, and each workgroup's sums for dw and db over its rows.  The weight of a row
 // of more than a wave is kept in LDS, which leaves those registers to the next row.
-template <bool BF, bool EVEN, int L, int R, bool NT>
+template <bool BF, RowEnd END, int L, int R, bool NT>
 __global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(NormCall c) {
     constexpr int V = BF ? 8 : 4, THREADS = grad_threads<BF, L>(), TEAMS = THREADS / L;
     constexpr bool WIDE = L > 64;
@@ -356,14 +360,14 @@ __global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(Norm
     // the weight, then the teams' sums
     __shared__ __align__(16) float held[WIDE ? L * R * V : THREADS * R * V];
     const int l = threadIdx.x % L, team = team_of<L>();
-    const Share<BF, EVEN, L, R> s(l, c.cols);
+    const Share<BF, END, L, R> s(l, c.cols);
     // (a wide row's values: 16 bytes of a lane beside those of the next)
     auto held_at = [&](int i, int e) { return ((i * (V / 4) + e / 4) * L + l) * 4 + e % 4; };
     float w[WIDE ? 1 : R][V], dw[R][V], db[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
         float v[V];
-        load_weight<V, EVEN || L >= 64>(c.weight, c.weight_bf16, s.at[i], c.cols, 1.f, v);
+        load_weight<V, END != kShort>(c.weight, c.weight_bf16, s.at[i], c.cols, 1.f, v);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             if (!WIDE)
@@ -377,7 +381,7 @@ __global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(Norm
     TeamSum<L, THREADS> sum(red);
     const float n = (float)c.cols;
     struct Buffer {
-        Row<BF, EVEN, L, R> x, dy;
+        Row<BF, END, L, R> x, dy;
         float mean, rstd;
     };
     auto load = [&](Buffer& r, int64_t first) {
@@ -400,7 +404,7 @@ __global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(Norm
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 float d = r.dy.u[i].at(e);
-                if (!EVEN && L >= 64 && s.maybe(i)) d = s.mine(i, e, c.cols) ? d : 0.f;
+                if (END == kShifted && s.maybe(i)) d = s.mine(i, e, c.cols) ? d : 0.f;
                 const float t = r.x.u[i].at(e) - mu, g = d * weight(i, e);
                 dw[i][e] = fmaf(d * rs, t, dw[i][e]);
                 db[i][e] += d;
@@ -411,7 +415,7 @@ __global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(Norm
         sum(s1, s2, c.center);
         // dx = rstd g - rstd^3 (x - mean) sum(g (x - mean)) / C - rstd sum(g) / C
         const float a = -(s1 * rs / n) * rs * rs, b = c.center ? -(s2 / n) * rs : 0.f;
-        const Out<BF, EVEN, L, R> out(c.out, has ? row_at(row, c.heads, c.out_token, c.out_head) : 0, c.cols, has);
+        const Out<BF, END, L, R> out(c.out, has ? row_at(row, c.heads, c.out_token, c.out_head) : 0, c.cols, has);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             float o[V];
@@ -493,47 +497,78 @@ __global__ __launch_bounds__(1024) void norm_grad_join_kernel(NormCall c, int bl
     put_grad(out, c.grad_bf16, c.accumulate, col, s);
 }
 
-// Calls fn(lanes of a team, units a lane) for a row of `units` 16-byte units.
-template <bool BF, class F>
+// Calls fn(lanes of a team, units a lane) for a row of `units` 16-byte units: the
+// smallest L * R that holds them, and lanes with at most 32 values each.  More
+// units a lane rather than more waves a team, which meet at a barrier (120 MB of
+// bf16 rows of 1536 columns on 192 lanes 52 us, on 64 lanes 41), and three units
+// rather than four where they do, which leaves fewer lanes idle (rows of 2049
+// columns on 256 lanes of two 65 us, on 128 of three 48).
+template <bool BF, RowEnd END, class F>
 hipError_t with_team(int units, F&& fn) {
     using std::integral_constant;
-#define MUON_TEAM(L, R) fn(integral_constant<int, L>{}, integral_constant<int, R>{})
-    if (units <= 8) return MUON_TEAM(8, 1);
-    if (units <= 16) return MUON_TEAM(16, 1);
-    if (units <= 32) return MUON_TEAM(32, 1);
-    if (units <= 64) return MUON_TEAM(64, 1);
-    if (units <= 128) return MUON_TEAM(64, 2);
-    if (units <= 256) return MUON_TEAM(256, 1);
-    if (units <= 512) return MUON_TEAM(256, 2);
-    if (units <= 1024) return MUON_TEAM(256, 4);
-    if constexpr (!BF)
-        if (units > 2048) return MUON_TEAM(512, 8);
-    return MUON_TEAM(512, 4);
-#undef MUON_TEAM
+#define MUON_TEAM(L, R) \
+    if (units <= L * R) return fn(integral_constant<int, L>{}, integral_constant<int, R>{})
+    MUON_TEAM(8, 1);
+    if constexpr (END != kShort) {
+        MUON_TEAM(16, 1);
+        MUON_TEAM(32, 1);
+        MUON_TEAM(16, 3);
+        MUON_TEAM(64, 1);
+        MUON_TEAM(32, 3);
+        MUON_TEAM(64, 2);
+        MUON_TEAM(64, 3);
+        MUON_TEAM(64, 4);
+        MUON_TEAM(128, 3);
+        MUON_TEAM(128, 4);
+        MUON_TEAM(192, 4);
+        MUON_TEAM(256, 4);
+        MUON_TEAM(384, 4);
+        MUON_TEAM(512, 4);
+        if constexpr (!BF) {
+            MUON_TEAM(384, 8);
+            MUON_TEAM(512, 8);
+        }
+    }
+    return hipErrorInvalidValue;  // (no row is longer)
 }
 
 // The same for the gradient, whose sums for dw and db take two registers a value:
-// at most 16 values a lane.
-template <bool BF, class F>
+// at most 24 values a lane.  (120 MB of fp32 rows of 1000 columns: 256 lanes of one
+// unit 63 us, 64 of four 66; of 2047: 256 of two 68, 128 of four 73.)
+template <bool BF, RowEnd END, class F>
 hipError_t with_grad_team(int units, F&& fn) {
     using std::integral_constant;
-#define MUON_TEAM(L, R) fn(integral_constant<int, L>{}, integral_constant<int, R>{})
-    if (units <= 8) return MUON_TEAM(8, 1);
-    if (units <= 16) return MUON_TEAM(16, 1);
-    if (units <= 32) return MUON_TEAM(32, 1);
-    if (units <= 64) return MUON_TEAM(64, 1);
-    if (units <= 128) return MUON_TEAM(64, 2);
-    if (units <= 256) return MUON_TEAM(256, 1);
-    if (units <= 512) return MUON_TEAM(256, 2);
-    if constexpr (BF) {
-        if (units <= 1024) return MUON_TEAM(512, 2);
-        return MUON_TEAM(1024, 2);
-    } else {
-        if (units <= 1024) return MUON_TEAM(256, 4);
-        if (units <= 2048) return MUON_TEAM(512, 4);
-        return MUON_TEAM(1024, 4);
+    MUON_TEAM(8, 1);
+    if constexpr (END != kShort) {
+        MUON_TEAM(16, 1);
+        MUON_TEAM(32, 1);
+        MUON_TEAM(16, 3);
+        MUON_TEAM(64, 1);
+        MUON_TEAM(32, 3);
+        MUON_TEAM(64, 2);
+        if constexpr (BF) {
+            MUON_TEAM(128, 2);
+            MUON_TEAM(192, 2);
+            MUON_TEAM(256, 2);
+            MUON_TEAM(384, 2);
+            MUON_TEAM(512, 2);
+            MUON_TEAM(768, 2);
+            MUON_TEAM(1024, 2);
+        } else {
+            MUON_TEAM(64, 3);
+            MUON_TEAM(256, 1);
+            MUON_TEAM(192, 2);
+            MUON_TEAM(256, 2);
+            MUON_TEAM(192, 4);
+            MUON_TEAM(256, 4);
+            MUON_TEAM(384, 4);
+            MUON_TEAM(512, 4);
+            MUON_TEAM(768, 4);
+            MUON_TEAM(1024, 4);
+        }
     }
 #undef MUON_TEAM
+    return hipErrorInvalidValue;
 }
 
 int units_of(int cols, bool bf) { return (cols + (bf ? 7 : 3)) / (bf ? 8 : 4); }
@@ -550,25 +585,30 @@ NormCall with_loads(NormCall c) {
     return c;
 }
 
+// Calls fn(whether rows are bf16, how they end).
 template <class F>
 hipError_t with_types(const NormCall& c, F&& fn) {
-    const bool even = c.cols % (c.bf16 ? 8 : 4) == 0;
-    if (c.bf16) return even ? fn(std::true_type{}, std::true_type{}) : fn(std::true_type{}, std::false_type{});
-    return even ? fn(std::false_type{}, std::true_type{}) : fn(std::false_type{}, std::false_type{});
+    using std::integral_constant;
+    auto with = [&](auto bf) {
+        constexpr int V = bf.value ? 8 : 4;
+        if (c.cols % V == 0) return fn(bf, integral_constant<RowEnd, kWhole>{});
+        return c.cols > V ? fn(bf, integral_constant<RowEnd, kShifted>{}) : fn(bf, integral_constant<RowEnd, kShort>{});
+    };
+    return c.bf16 ? with(std::true_type{}) : with(std::false_type{});
 }
 
 }  // namespace
 
 hipError_t launch_norm_forward(const NormCall& call, int cus, hipStream_t st) {
     const NormCall c = with_loads(call);
-    return with_types(c, [&](auto bf, auto even) {
-        return with_team<bf.value>(units_of(c.cols, c.bf16), [&](auto l, auto r) {
+    return with_types(c, [&](auto bf, auto end) {
+        return with_team<bf.value, end.value>(units_of(c.cols, c.bf16), [&](auto l, auto r) {
             constexpr int NT = threads_of<l.value>();
-            const int blocks = blocks_for(c.rows, NT / l.value, cus, NT > 256 ? 2 : 8);
+            const int blocks = blocks_for(c.rows, NT / l.value, cus, NT > 256 ? 2 : 2048 / NT);
             if (l.value < 64 && c.nontemporal)
-                norm_forward_kernel<bf.value, even.value, l.value, r.value, l.value < 64><<<blocks, NT, 0, st>>>(c);
+                norm_forward_kernel<bf.value, end.value, l.value, r.value, l.value < 64><<<blocks, NT, 0, st>>>(c);
             else
-                norm_forward_kernel<bf.value, even.value, l.value, r.value, false><<<blocks, NT, 0, st>>>(c);
+                norm_forward_kernel<bf.value, end.value, l.value, r.value, false><<<blocks, NT, 0, st>>>(c);
             return hipGetLastError();
         });
     });
@@ -579,12 +619,12 @@ int norm_grad_blocks(int32_t rows, int32_t cols, bool bf16, int cus) {
     auto count = [&](auto bf, auto l, auto r) {
         constexpr int NT = grad_threads<bf.value, l.value>();
         // as many as registers leave room for
-        blocks = blocks_for(rows, NT / l.value, cus, NT > 512 ? 1 : NT > 256 || r.value > 1 ? 2 : 4);
+        blocks = blocks_for(rows, NT / l.value, cus, l.value > 64 ? std::max(1, 1024 / NT) : r.value > 1 ? 2 : 4);
         return hipSuccess;
     };
     const int units = units_of(cols, bf16);
-    (void)(bf16 ? with_grad_team<true>(units, [&](auto l, auto r) { return count(std::true_type{}, l, r); })
-                : with_grad_team<false>(units, [&](auto l, auto r) { return count(std::false_type{}, l, r); }));
+    (void)(bf16 ? with_grad_team<true, kWhole>(units, [&](auto l, auto r) { return count(std::true_type{}, l, r); })
+                : with_grad_team<false, kWhole>(units, [&](auto l, auto r) { return count(std::false_type{}, l, r); }));
     return blocks;
 }
 
@@ -592,13 +632,13 @@ hipError_t launch_norm_grad(const NormCall& call, int cus, hipStream_t st) {
     const NormCall c = with_loads(call);
     const int blocks = norm_grad_blocks(c.rows, c.cols, c.bf16, cus);
     hipError_t e = hipSuccess;
-    if (blocks > 0) e = with_types(c, [&](auto bf, auto even) {
-        return with_grad_team<bf.value>(units_of(c.cols, c.bf16), [&](auto l, auto r) {
+    if (blocks > 0) e = with_types(c, [&](auto bf, auto end) {
+        return with_grad_team<bf.value, end.value>(units_of(c.cols, c.bf16), [&](auto l, auto r) {
             constexpr int NT = grad_threads<bf.value, l.value>();
             if (l.value < 64 && c.nontemporal)
-                norm_grad_kernel<bf.value, even.value, l.value, r.value, l.value < 64><<<blocks, NT, 0, st>>>(c);
+                norm_grad_kernel<bf.value, end.value, l.value, r.value, l.value < 64><<<blocks, NT, 0, st>>>(c);
             else
-                norm_grad_kernel<bf.value, even.value, l.value, r.value, false><<<blocks, NT, 0, st>>>(c);
+                norm_grad_kernel<bf.value, end.value, l.value, r.value, false><<<blocks, NT, 0, st>>>(c);
             return hipGetLastError();
         });
     });

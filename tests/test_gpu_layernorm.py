@@ -75,8 +75,8 @@ def _forward(x, w=None, b=None, eps=1e-5, center=True, out=None, **kw):
     return y, mean, rstd
 
 
-COLS = [1, 2, 7, 8, 31, 33, 64, 65, 128, 129, 250, 256, 257, 511, 512, 513, 1000, 1001, 1024, 1025, 2048, 2049, 4096,
-        4097, 7168, 8192, 8193, 16383, 16384]
+COLS = [1, 2, 3, 4, 5, 7, 8, 9, 15, 31, 33, 64, 65, 128, 129, 250, 256, 257, 511, 512, 513, 1000, 1001, 1024, 1025, 2048, 2049, 4096,
+        4097, 7168, 8192, 8193, 16383, 16384, 100, 600, 769, 1536, 1537, 2560, 2999, 5120, 6145, 10000, 12288, 12289]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
