@@ -768,18 +768,34 @@ def muon_qk_smax(h, q, k, cu_q, cu_k, smax_q, workspace, smax_k=None, scale=None
                                _stream_on(stream, dev, h)), "muon_qk_smax")
 
 
-def _queue(h, stream, *tensors):
+# What the bindings below ask torch for in every call (torch is imported with the
+# first one): a small call's time is the host's, so they look at each tensor once.
+_torch = None
+
+
+def _torch_parts():
+    """(float32, int32, float64, {type: muon_dtype}, device index -> its current stream)"""
+    global _torch
+    import torch
+    _torch = (torch.float32, torch.int32, torch.float64, {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16},
+              torch._C._cuda_getCurrentRawStream)
+    return _torch
+
+
+def _elsewhere(h, stream, tensors):
+    """Says which of the tensors is not on the handle's device."""
+    _stream_on(stream, _same_device(*tensors), h)
+    raise ValueError("expected tensors on device %s" % h.device)
+
+
+def _queue(h, stream, current, tensors):
     """The stream to launch on, once every tensor (None among them: not given) is
-    known to be on the handle's device.  (One look at each: a small call's time is
-    the host's.)"""
+    known to be on the handle's device."""
     i = h.device
     for t in tensors:
         if t is not None and t.get_device() != i:
-            _stream_on(stream, _same_device(*tensors), h)  # says which of them is where
-    if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(i)
-    return _stream_on(stream, tensors[0].device, h)
+            _elsewhere(h, stream, tensors)
+    return current(i) if stream is None else _stream_on(stream, tensors[0].device, h)
 
 
 def _heads(t, shape, what):
@@ -812,13 +828,20 @@ def _vector(t, numel, dtype, what):
     return t.data_ptr()
 
 
-def _pair(a, b, numel, what):
+def _kind(kinds, dtype):
+    k = kinds.get(dtype)
+    if k is None:
+        raise TypeError("only float32 and bfloat16 tensors are supported, got %s" % dtype)
+    return k
+
+
+def _pair(a, b, numel, kinds, what):
     """(pointer, pointer, type) of two vectors of one type, either may be None."""
     t = a if a is not None else b
     if t is None:
         return None, None, MUON_F32
     dtype = t.dtype
-    return _vector(a, numel, dtype, what), _vector(b, numel, dtype, what), _dt(t)
+    return _vector(a, numel, dtype, what), _vector(b, numel, dtype, what), _kind(kinds, dtype)
 
 
 def muon_layernorm_forward(h, x, y, weight=None, bias=None, mean=None, rstd=None, eps=1e-5, center=True,
@@ -828,24 +851,27 @@ def muon_layernorm_forward(h, x, y, weight=None, bias=None, mean=None, rstd=None
     bias; ``y`` may be ``x`` itself.  ``mean`` and ``rstd`` (float32, one value per
     row; optional) receive the statistics that :func:`muon_layernorm_grad` reads.
     Without ``center`` the mean is taken as zero (root mean square norm)."""
-    import torch
-    queue = _queue(h, stream, x, y, weight, bias, mean, rstd)
-    shape = x.shape
-    if y.shape != shape or y.dtype is not x.dtype:
+    f32, _, _, kinds, current = _torch or _torch_parts()
+    queue = _queue(h, stream, current, (x, y, weight, bias, mean, rstd))
+    shape, dtype = x.shape, x.dtype
+    if not y.is_same_size(x) or y.dtype is not dtype:
         raise ValueError("x and y differ in shape or type")
-    hx, hy, cols = _heads(x, shape, "x"), _heads(y, shape, "y"), shape[-1]
-    pw, pb, wide = _pair(weight, bias, cols, "weight and bias")
-    rows, f32 = shape[0] * hx.heads, torch.float32
-    n = MuonLayernorm(pw, pb, shape[0], cols, _dt(x), wide, 1 if center else 0, eps)
-    _check(load().muon_layernorm_forward(h, n, hx, hy, _vector(mean, rows, f32, "mean"),
-                                         _vector(rstd, rows, f32, "rstd"), queue), "muon_layernorm_forward")
+    hx, cols = _heads(x, shape, "x"), shape[-1]
+    pw, pb, wide = _pair(weight, bias, cols, kinds, "weight and bias")
+    rows = shape[0] * hx.heads
+    st = (_lib or load()).muon_layernorm_forward(
+        h, MuonLayernorm(pw, pb, shape[0], cols, _kind(kinds, dtype), wide, 1 if center else 0, eps), hx,
+        _heads(y, shape, "y"), _vector(mean, rows, f32, "mean"), _vector(rstd, rows, f32, "rstd"), queue)
+    if st:
+        _check(st, "muon_layernorm_forward")
 
 
 def muon_layernorm_workspace_size(h, x):
     """Workspace bytes of :func:`muon_layernorm_grad` for an ``x`` of this shape and type."""
     sz = ctypes.c_size_t()
     n = MuonLayernorm(None, None, x.shape[0], x.shape[-1], _dt(x), MUON_F32, 1, 0.0)
-    _check(load().muon_layernorm_workspace_size(h, n, _heads(x, x.shape, "x").heads, sz), "muon_layernorm_workspace_size")
+    _check(load().muon_layernorm_workspace_size(h, n, _heads(x, x.shape, "x").heads, sz),
+           "muon_layernorm_workspace_size")
     return sz.value
 
 
@@ -855,23 +881,25 @@ def muon_layernorm_grad(h, x, dy, rstd, workspace, mean=None, weight=None, dx=No
     ``center``) and ``rstd``: ``dx`` (which may be ``x`` or ``dy`` itself), and
     ``dweight`` and ``dbias`` of one type, added to what they hold with
     ``accumulate``.  Each is optional."""
-    import torch
-    queue = _queue(h, stream, x, dy, rstd, workspace, mean, weight, dx, dweight, dbias)
+    f32, _, _, kinds, current = _torch or _torch_parts()
+    queue = _queue(h, stream, current, (x, dy, rstd, workspace, mean, weight, dx, dweight, dbias))
     shape, dtype = x.shape, x.dtype
-    for t in (dy, dx):
-        if t is not None and (t.shape != shape or t.dtype is not dtype):
-            raise ValueError("x, dy and dx differ in shape or type")
+    if not dy.is_same_size(x) or dy.dtype is not dtype or \
+            (dx is not None and (not dx.is_same_size(x) or dx.dtype is not dtype)):
+        raise ValueError("x, dy and dx differ in shape or type")
     if center and mean is None:
         raise ValueError("a centered norm needs its mean")
-    hx, cols, f32 = _heads(x, shape, "x"), shape[-1], torch.float32
+    hx, cols = _heads(x, shape, "x"), shape[-1]
     rows = shape[0] * hx.heads
-    pw, _, wide = _pair(weight, None, cols, "weight")
-    pdw, pdb, grad = _pair(dweight, dbias, cols, "dweight and dbias")
-    n = MuonLayernorm(pw, None, shape[0], cols, _dt(x), wide, 1 if center else 0, 0.0)
-    _check(load().muon_layernorm_grad(
-        h, n, hx, _heads(dy, shape, "dy"), _vector(mean, rows, f32, "mean"), _vector(rstd, rows, f32, "rstd"),
-        _heads(dx, shape, "dx") if dx is not None else None, pdw, pdb, grad, 1 if accumulate else 0, workspace.data_ptr(),
-        _nbytes(workspace), queue), "muon_layernorm_grad")
+    pw, _, wide = _pair(weight, None, cols, kinds, "weight")
+    pdw, pdb, grad = _pair(dweight, dbias, cols, kinds, "dweight and dbias")
+    st = (_lib or load()).muon_layernorm_grad(
+        h, MuonLayernorm(pw, None, shape[0], cols, _kind(kinds, dtype), wide, 1 if center else 0, 0.0), hx,
+        _heads(dy, shape, "dy"), _vector(mean, rows, f32, "mean"), _vector(rstd, rows, f32, "rstd"),
+        _heads(dx, shape, "dx") if dx is not None else None, pdw, pdb, grad, 1 if accumulate else 0,
+        workspace.data_ptr(), _nbytes(workspace), queue)
+    if st:
+        _check(st, "muon_layernorm_grad")
 
 
 def muon_rotary_frequencies(pairs, base=10000.0, scaling="none", factor=1.0, context=0.0, low=1.0, high=32.0):
@@ -894,38 +922,41 @@ def muon_rotary(h, x, y, positions, frequencies, first=0, interleaved=False, sca
     :func:`muon_rotary_frequencies`), the pairs neighbours with ``interleaved``,
     else half the turning part apart; other elements are copied.  ``transpose``
     turns back: dx from dy."""
-    import torch
+    _, i32, f64, kinds, current = _torch or _torch_parts()
     xs = x if isinstance(x, (list, tuple)) else (x,)
     ys = y if isinstance(y, (list, tuple)) else (y,)
     n = len(xs)
     if n != len(ys) or not 1 <= n <= 4:
         raise ValueError("expected one to four tensors and as many outputs")
-    queue = _queue(h, stream, positions, frequencies, *xs, *ys)
+    queue = _queue(h, stream, current, (positions, frequencies, *xs, *ys))
     x0, pairs = xs[0], frequencies.numel()
     shape, dtype = x0.shape, x0.dtype
     tokens, dim = shape[0], shape[-1]
     hx, hy = [], []
     for a, b in zip(xs, ys):
-        shape = a.shape
-        if b.shape != shape or shape[0] != tokens or shape[-1] != dim or a.dtype is not dtype or b.dtype is not dtype:
+        if a is not x0:
+            shape = a.shape
+        if not b.is_same_size(a) or shape[0] != tokens or shape[-1] != dim or a.dtype is not dtype or \
+                b.dtype is not dtype:
             raise ValueError("the tensors differ in tokens, head size or type, or from their outputs in shape")
         hx.append(_heads(a, shape, "x"))
         hy.append(_heads(b, shape, "y"))
     hs = _HEADS_OF[n]
-    p = MuonPositions(_vector(positions, tokens, torch.int32, "positions"),
-                      _vector(frequencies, pairs, torch.float64, "frequencies"), tokens, dim, first, pairs,
-                      1 if interleaved else 0, _dt(x0), scale)
-    _check(load().muon_rotary(h, p, hs(*hx), hs(*hy), n, 1 if transpose else 0, queue), "muon_rotary")
+    p = MuonPositions(_vector(positions, tokens, i32, "positions"), _vector(frequencies, pairs, f64, "frequencies"),
+                      tokens, dim, first, pairs, 1 if interleaved else 0, _kind(kinds, dtype), scale)
+    st = (_lib or load()).muon_rotary(h, p, hs(*hx), hs(*hy), n, 1 if transpose else 0, queue)
+    if st:
+        _check(st, "muon_rotary")
 
 
-def _router(logits, top_k, renormalize):
+def _router(logits, top_k, kinds, renormalize):
     if logits.dim() != 2:
         raise ValueError("logits must be 2D")
     (tokens, experts), (ld, step) = logits.shape, logits.stride()
     if step != 1 and experts > 1:
         raise ValueError("logits need unit column stride")
-    return MuonRouter(logits.data_ptr(), tokens, ld if tokens > 1 else experts, experts, top_k, _dt(logits),
-                      1 if renormalize else 0), tokens, experts
+    return MuonRouter(logits.data_ptr(), tokens, ld if tokens > 1 else experts, experts, top_k,
+                      _kind(kinds, logits.dtype), 1 if renormalize else 0), tokens, experts
 
 
 def _top_k(chosen):
@@ -937,7 +968,8 @@ def _top_k(chosen):
 def muon_router_workspace_size(h, logits, top_k):
     """Workspace bytes of :func:`muon_router_forward` for logits of this shape."""
     sz = ctypes.c_size_t()
-    _check(load().muon_router_workspace_size(h, _router(logits, top_k, False)[0], sz), "muon_router_workspace_size")
+    r = _router(logits, top_k, (_torch or _torch_parts())[3], False)[0]
+    _check(load().muon_router_workspace_size(h, r, sz), "muon_router_workspace_size")
     return sz.value
 
 
@@ -951,38 +983,41 @@ def muon_router_forward(h, logits, chosen, gates, counts, offsets, workspace, ro
     choice's row in the groups, and ``order`` (tokens * top_k), its inverse, so that
     ``x[order // top_k]`` is grouped by expert; ``live`` (1 int32), the tokens that
     have a logit above -inf; ``losses`` (2 float32): the balance and the z loss."""
-    import torch
-    i32, f32 = torch.int32, torch.float32
-    queue = _queue(h, stream, logits, chosen, gates, counts, offsets, workspace, rows, order, live, losses)
-    top_k, shape = _top_k(chosen), chosen.shape
-    r, tokens, experts = _router(logits, top_k, renormalize)
+    f32, i32, _, kinds, current = _torch or _torch_parts()
+    queue = _queue(h, stream, current, (logits, chosen, gates, counts, offsets, workspace, rows, order, live, losses))
+    top_k = _top_k(chosen)
+    r, tokens, experts = _router(logits, top_k, kinds, renormalize)
     n = tokens * top_k
-    if gates.shape != shape or (rows is not None and rows.shape != shape):
+    if not gates.is_same_size(chosen) or (rows is not None and not rows.is_same_size(chosen)):
         raise ValueError("chosen, gates and rows differ in shape")
     out = MuonRouting(_vector(chosen, n, i32, "chosen"), _vector(gates, n, f32, "gates"),
                       _vector(counts, experts, i32, "counts"), _vector(offsets, experts + 1, i32, "offsets"),
                       _vector(rows, n, i32, "rows"), _vector(order, n, i32, "order"), _vector(live, 1, i32, "live"),
                       _vector(losses, 2, f32, "losses"))
-    _check(load().muon_router_forward(h, r, out, workspace.data_ptr(), _nbytes(workspace), queue),
-           "muon_router_forward")
+    st = (_lib or load()).muon_router_forward(h, r, out, workspace.data_ptr(), _nbytes(workspace), queue)
+    if st:
+        _check(st, "muon_router_forward")
 
 
 def muon_router_grad(h, logits, chosen, counts, live, dlogits, dgates=None, balance=0.0, z=0.0,
                      renormalize=False, stream=None):
     """``dlogits`` of sum(``dgates`` * gates) + ``balance`` * balance loss + ``z`` * z
     loss, with what :func:`muon_router_forward` gave."""
-    import torch
-    i32 = torch.int32
-    queue = _queue(h, stream, logits, chosen, counts, live, dlogits, dgates)
+    f32, i32, _, kinds, current = _torch or _torch_parts()
+    queue = _queue(h, stream, current, (logits, chosen, counts, live, dlogits, dgates))
     top_k = _top_k(chosen)
-    r, tokens, experts = _router(logits, top_k, renormalize)
-    if dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype or (experts > 1 and dlogits.stride(1) != 1):
-        raise ValueError("dlogits must have the logits' shape and type, and unit column stride")
+    r, tokens, experts = _router(logits, top_k, kinds, renormalize)
+    if not dlogits.is_same_size(logits) or dlogits.dtype is not logits.dtype:
+        raise ValueError("dlogits must have the logits' shape and type")
+    ld, step = dlogits.stride()
+    if step != 1 and experts > 1:
+        raise ValueError("dlogits need unit column stride")
     n = tokens * top_k
-    _check(load().muon_router_grad(h, r, _vector(chosen, n, i32, "chosen"), _vector(counts, experts, i32, "counts"),
-                                   _vector(live, 1, i32, "live"), _vector(dgates, n, torch.float32, "dgates"), balance,
-                                   z, dlogits.data_ptr(), dlogits.stride(0) if tokens > 1 else experts, queue),
-           "muon_router_grad")
+    st = (_lib or load()).muon_router_grad(
+        h, r, _vector(chosen, n, i32, "chosen"), _vector(counts, experts, i32, "counts"), _vector(live, 1, i32, "live"),
+        _vector(dgates, n, f32, "dgates"), balance, z, dlogits.data_ptr(), ld if tokens > 1 else experts, queue)
+    if st:
+        _check(st, "muon_router_grad")
 
 
 def muon_test_gram_bf16(h, X, A, m, n, ldx, lda, s2=1.0, stream=None):

@@ -359,4 +359,4 @@ def test_binding_describes_tensors():
         with pytest.raises(ValueError):
             _lib._vector(bad, 6, torch.float32, "w")
     with pytest.raises(ValueError):
-        _lib._router(t[0].t(), 1, False)
+        _lib._router(t[0].t(), 1, _lib._torch_parts()[3], False)
