@@ -228,7 +228,8 @@ muon_status adamw_step(muon_handle h, const adamw_tensor* ts, int n,
  * and a multiple of 128 columns, without QK-Clip or update_out, the last
  * update launch also applies the step and phase 5 records no launch).  The
  * scaled and clipped steps are recorded in the same phases; muon_grad_norm,
- * muon_grad_clip, the expert products and muon_qk_smax are not recorded. */
+ * muon_grad_clip, the expert products, muon_qk_smax and the operators around
+ * them are not recorded. */
 #define MUON_NUM_PHASES 7
 typedef struct {
     float ms[MUON_NUM_PHASES];     /* summed launch durations per phase */
