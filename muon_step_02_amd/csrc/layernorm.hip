@@ -343,10 +343,10 @@ __device__ __forceinline__ void put_grad(void* p, bool bf, int accumulate, int c
 }
 
 // Threads of the gradient's workgroups: 256, or two teams that are wider than a
-// wave, or one.  Each team adds its rows to sums of its own, and the workgroup hands on
-// one sum a column: fewer, wider workgroups leave less to join.
-// (A lane's fp32 rows take twice the registers: 128, which 1024 threads have, are
-// not enough for two teams of 512.)
+// wave, or one.  Each team adds its rows to sums of its own, and the workgroup hands
+// on one sum a column: fewer, wider workgroups leave less to join.  (A lane's fp32
+// rows take twice the registers: 128, which 1024 threads have, are not enough for
+// two teams of 512.)
 template <bool BF, int L>
 constexpr int grad_threads() { return L <= 64 ? 256 : L <= (BF ? 512 : 256) ? 2 * L : L; }
 
@@ -413,15 +413,16 @@ __global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(Norm
             }
         if (!c.out) return;
         sum(s1, s2, c.center);
-        // dx = rstd g - rstd^3 (x - mean) sum(g (x - mean)) / C - rstd sum(g) / C
-        const float a = -(s1 * rs / n) * rs * rs, b = c.center ? -(s2 / n) * rs : 0.f;
+        // dx = rstd (g - sum(g) / C - (x - mean) rstd sum(g xhat) / C); rstd^3 as a
+        // factor would leave fp32 for rows of tiny values
+        const float a = -(s1 * rs / n) * rs, b = c.center ? -(s2 / n) : 0.f;
         const Out<BF, END, L, R> out(c.out, has ? row_at(row, c.heads, c.out_token, c.out_head) : 0, c.cols, has);
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             float o[V];
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                o[e] = fmaf(r.dy.u[i].at(e) * weight(i, e), rs, fmaf(r.x.u[i].at(e) - mu, a, b));
+                o[e] = fmaf(r.x.u[i].at(e) - mu, a, fmaf(r.dy.u[i].at(e), weight(i, e), b)) * rs;
             out.put(i, s, o);
         }
     };

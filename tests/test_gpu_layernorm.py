@@ -404,3 +404,18 @@ def test_rows_far_apart():
     into = torch.as_strided(buf, (3, cols), (far, 1))
     got = _grad(x, *args[1:], True, dx=into)
     assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+@pytest.mark.parametrize("cols", [64, 100, 1000, 7168])
+def test_grad_of_tiny_and_of_huge_rows(cols):
+    # rstd^2 and rstd^3 leave fp32, dx does not
+    for size in (1e-25, 1e25):
+        gen = _gen(cols)
+        x, dy = (torch.randn(30, cols, generator=gen, device=DEV) for _ in range(2))
+        x *= size
+        rstd = torch.full((30,), 1.0 / size, device=DEV)
+        mean = x.double().mean(1).float()
+        args = x, dy, mean, rstd, _weights(gen, cols, F32)[0]
+        got = _grad(*args, True)
+        assert all(bool(torch.isfinite(t).all()) for t in got)
+        _check_grad(*args, True, *got)
