@@ -133,7 +133,9 @@ muon_status check_router(const muon_router* r) {
     if (r->experts < 1 || r->experts > kRouterMaxExperts || r->top_k < 1 || r->top_k > kRouterMaxChoices ||
         r->top_k > r->experts || !valid_dtype(r->dtype) || (r->renormalize != 0 && r->renormalize != 1))
         return MUON_ERR_INVALID_ARG;
-    if (r->tokens < 0 || r->tokens > kRouterMaxTokens || r->tokens > kMaxRows / r->top_k || r->ld < r->experts || r->ld > kMaxSpan) return MUON_ERR_INVALID_ARG;
+    if (r->tokens < 0 || r->tokens > kRouterMaxTokens || r->tokens > kMaxRows / r->top_k || r->ld < r->experts ||
+        r->ld > kMaxSpan)
+        return MUON_ERR_INVALID_ARG;
     if (r->tokens > 0 && r->ld > kMaxSpan / r->tokens) return MUON_ERR_INVALID_ARG;
     return MUON_OK;
 }

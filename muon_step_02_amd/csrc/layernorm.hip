@@ -534,8 +534,10 @@ hipError_t with_team(int units, F&& fn) {
 }
 
 // The same for the gradient, whose sums for dw and db take two registers a value:
-// at most 24 values a lane.  (120 MB of fp32 rows of 1000 columns: 256 lanes of one
-// unit 63 us, 64 of four 66; of 2047: 256 of two 68, 128 of four 73.)
+// at most 24 values a lane, and 16 in teams of several waves.  (120 MB of fp32 rows
+// of 1000 columns: 256 lanes of one unit 63 us, 64 of four 66; of 2047: 256 of two
+// 68, 128 of four 73; of 2560: 384 of two 65, 192 of four 78; of 8192: 1024 of two
+// 71, 512 of four 78.)
 template <bool BF, RowEnd END, class F>
 hipError_t with_grad_team(int units, F&& fn) {
     using std::integral_constant;
@@ -560,10 +562,10 @@ hipError_t with_grad_team(int units, F&& fn) {
             MUON_TEAM(256, 1);
             MUON_TEAM(192, 2);
             MUON_TEAM(256, 2);
-            MUON_TEAM(192, 4);
-            MUON_TEAM(256, 4);
-            MUON_TEAM(384, 4);
-            MUON_TEAM(512, 4);
+            MUON_TEAM(384, 2);
+            MUON_TEAM(512, 2);
+            MUON_TEAM(768, 2);
+            MUON_TEAM(1024, 2);
             MUON_TEAM(768, 4);
             MUON_TEAM(1024, 4);
         }

@@ -57,7 +57,8 @@ __device__ __forceinline__ int divided(int v, float inv) { return (int)(((float)
 // INTER: neighbours are pairs.  WHOLE: no unit is cut short; a unit's two runs of V
 // elements then lie half its part apart, so that the lanes of a load or store
 // follow each other (806 MB of fp32 heads with 128 elements copied and 32 pairs of
-// neighbours 156 us, 190 with the runs side by side, two units a thread each).  NT: loads around the caches.
+// neighbours 156 us, 190 with the runs side by side, two units a thread each).  NT:
+// loads around the caches.
 template <bool BF, bool INTER, bool WHOLE, bool NT>
 __global__ __launch_bounds__(kThreads) void rotary_kernel(RotaryCall c, RotaryPlaces places) {
     constexpr int V = BF ? 8 : 4;

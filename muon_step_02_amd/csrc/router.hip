@@ -334,7 +334,8 @@ __global__ __launch_bounds__(kThreads) void router_choose_kernel(RouterCall c, R
         bool done = false;
         if constexpr (L >= 16)
             if (c.top_k <= kFew)
-                done = take_few<L, C>(key, c.top_k, slots[wave * TEAMS + team], m.chosen + t * c.top_k, m.gates + t * c.top_k);
+                done = take_few<L, C>(key, c.top_k, slots[wave * TEAMS + team], m.chosen + t * c.top_k,
+                                      m.gates + t * c.top_k);
         for (int j = 0; j < (done ? 0 : c.top_k); ++j) {
             int32_t top;
             const int i = take<L, C>(key, top);
@@ -571,8 +572,8 @@ __global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradCall c)
                 for (int k = 0; k < n_of; ++k) {
                     const int from = (lane - l + k) << 2;
                     const int to = L > 1 ? __builtin_amdgcn_ds_bpermute(from, e[q]) : e[q];
-                    const float v = L > 1 ? __builtin_bit_cast(float, __builtin_amdgcn_ds_bpermute(from, __builtin_bit_cast(int, d[q])))
-                                          : d[q];
+                    const int bits = __builtin_bit_cast(int, d[q]);
+                    const float v = __builtin_bit_cast(float, L > 1 ? __builtin_amdgcn_ds_bpermute(from, bits) : bits);
 #pragma unroll
                     for (int i = 0; i < C; ++i) own[i] += l * C + i == to ? v : 0.f;
                 }

@@ -12,9 +12,9 @@ __device__ __forceinline__ uint32_t lane_move(uint32_t v) {
     return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
 
-// (T: 32 bits.)  The two halves of a team of 2 * HALF lanes, each already alike in all its
-// lanes, brought to every lane: op(own, other).  Every lane of the wave has to
-// be active.  Within 16 lanes by lane moves (neighbours, pairs, mirrored
+// The two halves of a team of 2 * HALF lanes, each already alike in all its lanes,
+// brought to every lane: op(own, other), T of 32 bits.  Every lane of the wave has
+// to be active.  Within 16 lanes by lane moves (neighbours, pairs, mirrored
 // halves and rows), beyond by v_permlane16_swap and v_permlane32_swap.
 template <int HALF, class T, class F>
 __device__ __forceinline__ T team_step(T v, F&& op) {
