@@ -238,3 +238,32 @@ def test_tokens_far_apart():
     want = _turn(small, pos, freq)
     assert torch.equal(_turn(x, pos, freq, out=torch.zeros_like(small)), want)
     assert torch.equal(_turn(x, pos, freq, out=x), want)
+
+
+# parts that end within a unit of 4 or 8, that have just one, or less than one
+CUT = [(80, 0, 10, 3), (80, 5, 10, 300), (200, 0, 61, 70), (200, 9, 61, 129), (32, 8, 8, 5), (30, 8, 9, 5), (28, 4, 8, 2),
+       (31, 8, 8, 65), (41, 15, 9, 40), (36, 16, 4, 40), (24, 0, 12, 513), (18, 0, 7, 600), (60, 0, 5, 200), (4096, 0, 2047, 3)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,first,pairs,heads", CUT)
+def test_parts_that_end_within_a_unit(dim, first, pairs, heads, interleaved, dtype):
+    gen, freq = _gen(dim + pairs), mu.muon_rotary_frequencies(pairs)
+    kw = dict(first=first, interleaved=interleaved)
+    for tokens, pad, shift in ((1, 0, 0), (83, 3, 1)):
+        x, pos = _values(gen, tokens, heads, dim, dtype, pad, shift), _positions(gen, tokens)
+        y = _turn(x, pos, freq, **kw)
+        _check(x, y, pos, freq, **kw)
+        # in place, in a tensor whose other elements stay as they were
+        buf = torch.full((tokens, heads, dim + 3), 5.0, device=DEV, dtype=dtype)
+        buf[..., 1:1 + dim] = x
+        into = buf[..., 1:1 + dim]
+        for _ in range(2):
+            assert torch.equal(_turn(into, pos, freq, out=into, **kw), y)
+            into.copy_(x)
+        assert bool((buf[..., 0] == 5).all()) and bool((buf[..., 1 + dim:] == 5).all())
+        # one tensor in place beside one that is copied
+        into, other = x.clone(), torch.full_like(x, 7.0)
+        mu.muon_rotary(Handle.get(), [into, x], [into, other], pos, freq.to(DEV), **kw)
+        assert torch.equal(into, y) and torch.equal(other, y)
