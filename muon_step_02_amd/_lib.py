@@ -930,12 +930,11 @@ def muon_rotary(h, x, y, positions, frequencies, first=0, interleaved=False, sca
         raise ValueError("expected one to four tensors and as many outputs")
     queue = _queue(h, stream, current, (positions, frequencies, *xs, *ys))
     x0, pairs = xs[0], frequencies.numel()
-    shape, dtype = x0.shape, x0.dtype
-    tokens, dim = shape[0], shape[-1]
+    shape0, dtype = x0.shape, x0.dtype
+    tokens, dim = shape0[0], shape0[-1]
     hx, hy = [], []
     for a, b in zip(xs, ys):
-        if a is not x0:
-            shape = a.shape
+        shape = shape0 if a is x0 else a.shape
         if not b.is_same_size(a) or shape[0] != tokens or shape[-1] != dim or a.dtype is not dtype or \
                 b.dtype is not dtype:
             raise ValueError("the tensors differ in tokens, head size or type, or from their outputs in shape")

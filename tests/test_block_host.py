@@ -360,3 +360,40 @@ def test_binding_describes_tensors():
             _lib._vector(bad, 6, torch.float32, "w")
     with pytest.raises(ValueError):
         _lib._router(t[0].t(), 1, _lib._torch_parts()[3], False)
+
+
+class _Recorder:
+    """In the library's place: the descriptors that a binding hands it."""
+
+    def __init__(self):
+        self.x, self.y = [], []
+
+    def muon_rotary(self, h, p, x, y, n, transpose, stream):
+        def row(t):
+            return t.data, t.token, t.head, t.heads
+        self.x, self.y = [row(x[i]) for i in range(n)], [row(y[i]) for i in range(n)]
+        return 0
+
+
+@pytest.fixture
+def recorder(monkeypatch):
+    """What the bindings describe, without a device: tensors of the host count as the handle's."""
+    from muon_step_02_amd import _lib
+    stub = _Recorder()
+    monkeypatch.setattr(_lib, "_torch", _lib._torch_parts()[:4] + (lambda device: 0,))
+    monkeypatch.setattr(_lib, "_lib", stub)
+    return stub
+
+
+@pytest.mark.parametrize("tokens", [1, 5])
+@pytest.mark.parametrize("names", ["q", "qk", "kq", "qkq", "kqk", "qkqk", "kqqk", "qqk", "qkkq"])
+def test_binding_describes_every_tensor_of_a_turn(recorder, names, tokens):
+    # the same input may be listed again: it is only read
+    h = ctypes.c_void_p()
+    h.device = torch.zeros(0).get_device()
+    given = {"q": torch.zeros(tokens, 16, 8), "k": torch.zeros(tokens, 2, 8)}
+    xs = [given[n] for n in names]
+    ys = [torch.zeros_like(t) for t in xs]
+    mu.muon_rotary(h, xs, ys, torch.zeros(tokens, dtype=torch.int32), torch.zeros(4, dtype=torch.float64))
+    for tensors, rows in ((xs, recorder.x), (ys, recorder.y)):
+        assert rows == [(t.data_ptr(), t.shape[1] * 8, 8, t.shape[1]) for t in tensors]

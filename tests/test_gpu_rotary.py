@@ -267,3 +267,17 @@ def test_parts_that_end_within_a_unit(dim, first, pairs, heads, interleaved, dty
         into, other = x.clone(), torch.full_like(x, 7.0)
         mu.muon_rotary(Handle.get(), [into, x], [into, other], pos, freq.to(DEV), **kw)
         assert torch.equal(into, y) and torch.equal(other, y)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("tokens", [1, 50])
+def test_an_input_that_is_listed_again(tokens, dtype):
+    gen, freq = _gen(11), mu.muon_rotary_frequencies(32)
+    q, k, pos = _values(gen, tokens, 16, 64, dtype), _values(gen, tokens, 2, 64, dtype), _positions(gen, tokens)
+    for xs in ([q, k, q], [k, q, k], [q, q, k, k], [k, q, q, k]):
+        guard = [torch.full((tokens + 2, x.shape[1], 64), 7.0, device=DEV, dtype=dtype) for x in xs]
+        ys = [t[1:-1] for t in guard]
+        mu.muon_rotary(Handle.get(), xs, ys, pos, freq.to(DEV))
+        for x, y, t in zip(xs, ys, guard):
+            _check(x, y, pos, freq)
+            assert bool((t[0] == 7).all()) and bool((t[-1] == 7).all())
