@@ -578,10 +578,10 @@ muon_status muon_router_forward(muon_handle h, const muon_router* r, const muon_
 /* dlogits (the logits' type, leading dimension ld_dlogits) of
  *   sum over choices of dgates * gates + balance * balance loss + z * z loss
  * with chosen, counts and live as muon_router_forward gave them (a choice outside
- * [0, experts) is none; one that is listed twice counts twice).  Counts are
- * constants: the balance loss reaches the logits through the probabilities
- * alone.  dgates (tokens x top_k) may be NULL: zeros.  Rejects as the forward
- * pass does, and balance or z that are not finite. */
+ * [0, experts) is none, and its dgates are not used; one that is listed twice
+ * counts twice).  Counts are constants: the balance loss reaches the logits
+ * through the probabilities alone.  dgates (tokens x top_k) may be NULL: zeros.
+ * Rejects as the forward pass does, and balance or z that are not finite. */
 muon_status muon_router_grad(muon_handle h, const muon_router* r, const int32_t* chosen,
                              const int32_t* counts, const int32_t* live, const float* dgates,
                              float balance, float z, void* dlogits, int64_t ld_dlogits, void* stream);

@@ -541,6 +541,8 @@ __global__ __launch_bounds__(kThreads) void router_grad_kernel(RouterGradCall c)
                 e[q] = there ? gld(c.chosen + t * c.top_k + j) : -1;
                 d[q] = there ? gld(c.dgates + t * c.top_k + j) : 0.f;
                 if (e[q] >= c.experts) e[q] = -1;
+                // (where there is no choice, dgates may be anything)
+                d[q] = e[q] >= 0 ? d[q] : 0.f;
             }
             if (c.renormalize) {
                 // the gates are a softmax over the chosen logits

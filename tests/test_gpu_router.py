@@ -446,3 +446,21 @@ def test_streams_and_a_captured_graph():
         for n in want:
             assert torch.equal(out[n], want[n]), n
         assert torch.equal(dz, _grad(z, want, d, 0.1, 0.1, True))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("experts,k", [(8, 3), (20, 6), (61, 12), (100, 8), (200, 8), (300, 32), (1024, 20)])
+def test_grad_of_the_gates_of_absent_choices_is_not_looked_at(experts, k, dtype):
+    # a caller who fills dgates by `order` leaves anything where there is no choice
+    z = _logits(13, 150, experts, dtype)
+    z[::3, 2:] = NEG                       # fewer experts left than choices
+    z[1::9] = NEG                          # padding
+    got = _route(z, k)
+    got["chosen"][2::5, 1] = experts + 3   # and choices out of range
+    none = (got["chosen"] < 0) | (got["chosen"] >= experts)
+    d = torch.randn(150, k, generator=_gen(6), device=DEV)
+    for renormalize in (False, True):
+        want = _grad(z, got, torch.where(none, 0.0, d), 0.1, 0.1, renormalize)
+        assert bool(torch.isfinite(want).all())
+        for value in (float("nan"), float("inf"), -float("inf"), 3e38):
+            assert torch.equal(_grad(z, got, torch.where(none, value, d), 0.1, 0.1, renormalize), want)
