@@ -45,9 +45,10 @@ muon_status check_heads(const muon_heads* t, int64_t tokens, int64_t width, int3
 // spaced, else with the gaps between a token's heads (or a head's tokens).
 Rect heads_rect(const muon_heads& t, int64_t tokens, int64_t width, int32_t dtype, bool write, int owner) {
     const size_t es = elem_bytes(dtype);
-    int64_t outer = tokens, so = t.token, inner = t.heads, si = t.head;
-    if (inner == 1) return rect_of(t.data, outer, width, so > 0 ? so : width, es, write, owner);
-    if (outer == 1) return rect_of(t.data, inner, width, si > 0 ? si : width, es, write, owner);
+    // (what is no stride apart is one)
+    int64_t outer = t.token > 0 ? tokens : 1, so = t.token, inner = t.head > 0 ? t.heads : 1, si = t.head;
+    if (inner == 1) return rect_of(t.data, outer, width, so, es, write, owner);
+    if (outer == 1) return rect_of(t.data, inner, width, si, es, write, owner);
     if (si > so) {
         std::swap(outer, inner);
         std::swap(so, si);

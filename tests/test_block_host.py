@@ -152,6 +152,33 @@ def test_norm_without_rows_is_done(lib, handle):
     assert _forward(lib, handle, _norm(tokens=0), x=_heads(None), y=_heads(None)) == OK
 
 
+@pytest.mark.parametrize("tokens,heads", [(100000, 1), (2, 1), (1, 4000), (50, 40)])
+def test_norm_rows_that_are_one_take_the_bytes_of_one(lib, handle, tokens, heads):
+    # (a handle of zeroes has no compute units: a call that is not refused launches no workgroup)
+    n, row, need = _norm(tokens=tokens, weight=None, bias=None), 64 * BUF, ctypes.c_size_t()
+    assert lib.muon_layernorm_workspace_size(handle, n, heads, need) == OK
+    out = tokens * heads * 16 * 4
+
+    def one(at):
+        return mu.MuonHeads(at, 0, 16 if heads == 1 else 0, heads)
+
+    def many(at):
+        return mu.MuonHeads(at, heads * 16, 16, heads)
+
+    def forward(at):
+        return lib.muon_layernorm_forward(handle, n, one(row), many(at), None, None, None) == OVERLAP
+
+    def back(at):
+        # x is one row, and dy another one 64 bytes behind it
+        return lib.muon_layernorm_grad(handle, n, one(row), one(row + 64), BUF, BUF, many(at), None, None, 0, 0, 2 * BUF,
+                                       need.value, None) == OVERLAP
+
+    assert not forward(row + 64) and not forward(row + 256) and not forward(row - out)
+    assert forward(row) and forward(row + 60) and forward(row - out + 4)
+    assert not back(row + 128) and not back(row + 1024) and not back(row - out)
+    assert back(row) and back(row + 64) and back(row + 124) and back(row - out + 4)
+
+
 # ---- rotary positions -------------------------------------------------------------
 
 def _turn(**over):
@@ -207,6 +234,19 @@ def test_rotary_overlaps_refused(lib, handle):
     big = _turn(tokens=1 << 16, head_dim=64, pairs=32)
     x, y = (_heads(at, token=wide * 64, head=64, heads=wide) for at in (1 << 42, 1 << 44))
     assert _rotary(lib, handle, big, x=[x], y=[y]) == INVALID
+
+
+def test_rotary_heads_that_are_one_take_the_bytes_of_one(lib, handle):
+    # a call whose grid no launch holds is refused for that, behind the check for overlaps
+    wide, row = 65536, 1 << 42
+    p = _turn(tokens=1 << 20, head_dim=wide, pairs=8)
+
+    def turn(at):
+        return _rotary(lib, handle, p, x=[mu.MuonHeads(row, 0, wide, 1)], y=[mu.MuonHeads(at, wide, wide, 1)])
+
+    assert turn(row + 4 * wide) == INVALID and turn(row - (4 * wide << 20)) == INVALID
+    for at in (row, row + 4 * wide - 4, row - (4 * wide << 20) + 4):
+        assert turn(at) == OVERLAP
 
 
 def test_frequencies_against_their_formulas():

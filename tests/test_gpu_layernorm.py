@@ -419,3 +419,20 @@ def test_grad_of_tiny_and_of_huge_rows(cols):
         got = _grad(*args, True)
         assert all(bool(torch.isfinite(t).all()) for t in got)
         _check_grad(*args, True, *got)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_row_for_every_token_next_to_its_output(dtype):
+    # a gradient as that of a sum, and its output right behind it in one buffer
+    tokens, cols = 500, 64
+    buf = _values(_gen(12), tokens + 2, cols, dtype=dtype).contiguous()
+    w, b = _weights(_gen(13), cols, F32)
+    one, out = buf[:1].expand(tokens, cols), buf[1:tokens + 1]
+    first, last = buf[0].clone(), buf[-1].clone()
+    _check_forward(one, w, b, 1e-5, True, *_forward(one, w, b, out=out))
+    x = _values(_gen(14), tokens, cols, dtype=dtype)
+    mean, rstd = (t.float() for t in _stats(x, 1e-5, True))
+    _check_grad(x, one, mean, rstd, w, True, *_grad(x, one, mean, rstd, w, True, dx=out))
+    assert torch.equal(buf[0], first) and torch.equal(buf[-1], last)
+    with pytest.raises(mu.MuonError, match="MUON_ERR_OVERLAP"):
+        _forward(one, w, b, out=buf[:tokens])
