@@ -790,8 +790,10 @@ def _elsewhere(h, stream, tensors):
 
 def _queue(h, stream, current, tensors):
     """The stream to launch on, once every tensor (None among them: not given) is
-    known to be on the handle's device."""
-    i = h.device
+    known to be on the handle's device, or on one where the handle names none."""
+    i = getattr(h, "device", None)
+    if i is None:
+        i = _same_device(*tensors).index
     for t in tensors:
         if t is not None and t.get_device() != i:
             _elsewhere(h, stream, tensors)

@@ -376,6 +376,16 @@ def test_binding_refuses_tensors_on_the_host():
         mu.muon_router_grad(h, x, x, x, x, x)
 
 
+def test_binding_takes_a_handle_that_does_not_name_its_device():
+    # as the step's calls do; the tensors are looked at all the same
+    x = torch.zeros(4, 8)
+    for call in (lambda h: mu.muon_layernorm_forward(h, x, x),
+                 lambda h: mu.muon_rotary(h, x, x, torch.zeros(4, dtype=torch.int32), torch.zeros(4, dtype=torch.float64)),
+                 lambda h: mu.muon_router_grad(h, x, x, x, x, x)):
+        with pytest.raises(ValueError):
+            call(ctypes.c_void_p())
+
+
 def test_binding_describes_tensors():
     from muon_step_02_amd import _lib
 

@@ -261,3 +261,15 @@ def test_two_handles_on_two_streams():
             assert torch.equal(getattr(a, n), getattr(b, n)), n
     finally:
         mu.muon_destroy(b.h)
+
+
+def test_a_handle_that_does_not_name_its_device():
+    import ctypes
+    a, b = Block(7), Block(7)
+    b.h = ctypes.c_void_p(a.h.value)
+    for block in (a, b):
+        block.forward()
+        block.back()
+    torch.cuda.synchronize()
+    for n in ("y", "qn", "smax", "chosen", "losses", "yr", "dlogits", "dx", "G"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
