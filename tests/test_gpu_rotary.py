@@ -281,3 +281,36 @@ def test_an_input_that_is_listed_again(tokens, dtype):
         for x, y, t in zip(xs, ys, guard):
             _check(x, y, pos, freq)
             assert bool((t[0] == 7).all()) and bool((t[-1] == 7).all())
+
+
+# parts that end evenly, within a unit (so that units share elements), and with one shorter than a unit
+AROUND = [(64, 0, 32), (80, 0, 10), (100, 8, 17), (100, 3, 17)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim,first,pairs", AROUND)
+def test_loads_around_the_caches_in_place_and_copied(dim, first, pairs, interleaved, dtype):
+    # from 112 MiB that a call reads on: in place the turning elements alone count
+    heads, size = (24, 3), torch.finfo(dtype).bits // 8
+    tokens = -(-(112 << 20) // (sum(heads) * 2 * pairs * size)) + 5
+    gen, freq = _gen(dim), mu.muon_rotary_frequencies(pairs).to(DEV)
+    q, k = (_values(gen, tokens, n, dim, dtype) for n in heads)
+    pos = _positions(gen, tokens)
+    kw = dict(first=first, interleaved=interleaved)
+    y = [torch.zeros_like(q), torch.zeros_like(k)]
+    mu.muon_rotary(Handle.get(), [q, k], y, pos, freq, **kw)
+    for a in range(0, tokens, tokens // 3):
+        cut = slice(a, a + 501)
+        for x, got in zip((q, k), y):
+            assert torch.equal(got[cut], _turn(x[cut], pos[cut].contiguous(), freq, **kw))
+    mu.muon_rotary(Handle.get(), [q, k], [q, k], pos, freq, **kw)
+    assert torch.equal(q, y[0]) and torch.equal(k, y[1])
+    # and back, in place: what is copied has not changed
+    mu.muon_rotary(Handle.get(), [q, k], [q, k], pos, freq, transpose=True, **kw)
+    one, two = _pairs(first, pairs, interleaved)
+    rest = torch.ones(dim, dtype=torch.bool, device=DEV)
+    rest[one] = rest[two] = False
+    for x, got in zip((q, k), y):
+        assert torch.equal(x[:700, :, rest], got[:700, :, rest]) and torch.equal(x[-700:, :, rest], got[-700:, :, rest])
+        _check(got[-700:], x[-700:], pos[-700:], freq, transpose=True, **kw)
