@@ -65,7 +65,7 @@ __device__ __forceinline__ int divided(int v, float inv) { return (int)(((float)
 // kShort: some part is shorter than the V pairs or elements that this needs, and is
 // read and written one by one.  (60 MB of bf16 heads of 128: 20 us.  kShifted, heads
 // of 80 with 10 pairs, 20, where ends one by one took 36; kShort, heads of 100 with
-// 17 pairs from their fourth element on, 31 instead of 42.)
+// 17 pairs from their fourth element on, 29.)
 enum Cut { kWhole, kShifted, kShort };
 
 // The first pair of the turning part's unit i, one that is not kWhole.
