@@ -189,7 +189,8 @@ __device__ __forceinline__ bool take_few(const int32_t* key, int k, int2* slots,
     row_turns([&](auto r) {
         // lane p sees lane p - r: with p >= r an expert before its own
         const int32_t other = (int32_t)lane_move<0x120 + r.value>((uint32_t)mine.x);
-        before += other > (place >= r.value ? mine.x - 1 : mine.x);
+        // (a lane without one has the lowest key, and what wraps round there is not used)
+        before += other > (place >= r.value ? (int32_t)((uint32_t)mine.x - 1u) : mine.x);
     });
     if (l < 16 && place < all && before < k) {
         chosen[before] = mine.y;
