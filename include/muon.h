@@ -447,11 +447,12 @@ typedef struct {
 /* y from x; mean and rstd (tokens * heads floats, by token, then head) are
  * written where they are not NULL.  Statistics are fp32 sums over a row held in
  * registers, the variance that of the differences from the mean; y is rounded
- * once.  (Differences whose squares sum beyond fp32 give rstd = 0.)  y may be x
- * itself (the same strides).  Rejects sizes or strides out of range, null or
- * misaligned pointers, and outputs that share memory with anything else of the
- * call (MUON_ERR_OVERLAP; strided ranges that cannot be told apart count as
- * shared). */
+ * once.  (Differences whose squares sum beyond fp32 give rstd = 0, values that
+ * themselves do a row without finite statistics; with eps = 0 differences whose
+ * squares vanish in fp32 give an infinite rstd.)  y may be x itself (the same
+ * strides).  Rejects sizes or strides out of range, null or misaligned pointers,
+ * and outputs that share memory with anything else of the call
+ * (MUON_ERR_OVERLAP; strided ranges that cannot be told apart count as shared). */
 muon_status muon_layernorm_forward(muon_handle h, const muon_layernorm* n, const muon_heads* x,
                                    const muon_heads* y, float* mean, float* rstd, void* stream);
 

@@ -436,3 +436,23 @@ def test_one_row_for_every_token_next_to_its_output(dtype):
     assert torch.equal(buf[0], first) and torch.equal(buf[-1], last)
     with pytest.raises(mu.MuonError, match="MUON_ERR_OVERLAP"):
         _forward(one, w, b, out=buf[:tokens])
+
+
+@pytest.mark.parametrize("cols", [64, 100, 1000, 7168])
+def test_rows_beyond_what_fp32_squares_and_sums(cols):
+    sign = torch.where(torch.arange(cols, device=DEV) % 2 == 0, 1.0, -1.0)
+    w, b = _weights(_gen(15), cols, F32)
+    x = _values(_gen(16), 40, cols)
+    want = _forward(x, w, b)
+    x[5] = 1e25 * sign              # squares beyond fp32
+    x[6] = 3e38                     # the sum itself
+    x[7] = 1e-25 * sign             # no squares left: eps alone
+    y, mean, rstd = _forward(x, w, b)
+    assert float(rstd[5]) == 0.0 and torch.equal(y[5], b)
+    assert not bool(torch.isfinite(mean[6])) and bool(torch.isnan(y[6]).all())
+    assert abs(float(rstd[7]) * 1e-5 ** 0.5 - 1.0) <= 4 * U
+    assert bool(((y[7] - b).abs() <= 2.0 ** -24 * b.abs() + 1e-20).all())
+    assert float(_forward(x[7:8], w, b, eps=0.0)[2]) == float("inf")
+    keep = [i for i in range(40) if i not in (5, 6, 7)]
+    for got, ref in zip((y, mean, rstd), want):
+        assert torch.equal(got[keep], ref[keep])
