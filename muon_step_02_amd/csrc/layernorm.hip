@@ -344,9 +344,10 @@ __device__ __forceinline__ void put_grad(void* p, bool bf, int accumulate, int c
 
 // Threads of the gradient's workgroups: 256, or two teams that are wider than a
 // wave, or one.  Each team adds its rows to sums of its own, and the workgroup hands
-// on one sum a column: fewer, wider workgroups leave less to join.  (A lane's fp32
-// rows take twice the registers: 128, which 1024 threads have, are not enough for
-// two teams of 512.)
+// on one sum a column: fewer, wider workgroups leave less to join.  Two fp32 teams of
+// 384 or 512 lanes were slower than one (120 MB of rows of 2049 columns 78 us instead
+// of 69, of 4096 68 instead of 65, of 3500 the same), and 1024 threads hold no two
+// wider ones.
 template <bool BF, int L>
 constexpr int grad_threads() { return L <= 64 ? 256 : L <= (BF ? 512 : 256) ? 2 * L : L; }
 
@@ -426,7 +427,11 @@ __global__ __launch_bounds__((grad_threads<BF, L>())) void norm_grad_kernel(Norm
             out.put(i, s, o);
         }
     };
-    // (1024 threads have 128 registers each: no room for two rows)
+    // (Workgroups of one team of 768 or 1024 lanes do not read ahead: with 128
+    // registers a lane a second row of four fp32 units has no room, one of two bf16
+    // units spills on 1024 lanes and gains nothing on 768, 83 us either way for 120 MB
+    // of rows of 12000 columns.  One of two fp32 units has room: 72 us instead of 74
+    // for rows of 7168 columns, 73.4 instead of 74.1 for 5120.)
     walk_rows<Buffer, L <= 512>((int64_t)blockIdx.x * TEAMS, (int64_t)gridDim.x * TEAMS, c.rows, load, work);
     // the teams' sums, added in their order
     auto put = [&](int side, float (&acc)[R][V], void* out) {
