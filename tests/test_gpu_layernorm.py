@@ -456,3 +456,18 @@ def test_rows_beyond_what_fp32_squares_and_sums(cols):
     keep = [i for i in range(40) if i not in (5, 6, 7)]
     for got, ref in zip((y, mean, rstd), want):
         assert torch.equal(got[keep], ref[keep])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [7, 33, 64, 100, 513, 1024, 1001, 2049, 7168])
+def test_bf16_weights_off_four_bytes(cols, dtype):
+    gen = _gen(cols)
+    w, b = (t[1:] for t in _weights(gen, cols + 1, BF16))
+    x = _values(gen, 41, cols, dtype=dtype)
+    _check_forward(x, w, b, 1e-5, True, *_forward(x, w, b))
+    held = torch.full((2, cols + 2), 7.0, device=DEV, dtype=BF16)
+    mean, rstd = (t.float() for t in _stats(x, 1e-5, True))
+    dy = _values(gen, 41, cols, dtype=dtype)
+    dw, db = held[0, 1:-1], held[1, 1:-1]
+    _check_grad(x, dy, mean, rstd, w, True, *_grad(x, dy, mean, rstd, w, True, dw=dw, db=db))
+    assert bool((held[:, 0] == 7).all()) and bool((held[:, -1] == 7).all())
